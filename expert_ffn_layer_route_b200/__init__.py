@@ -28,6 +28,15 @@ from ._native import (  # noqa: F401
     moe_grouped_ffn,
     moe_combine,
     moe_layer_forward,
+    GemmDesc,
+    moe_grouped_gemm,
+    moe_grouped_gemm_grad_x,
+    moe_grouped_gemm_grad_w,
+    moe_grouped_gemm_i8,
+    moe_quant_rows_i8,
+    moe_swiglu,
+    moe_swiglu_quant_i8,
+    moe_swiglu_grad,
     moe_status_string,
     moe_get_last_error,
     ExpertCache,

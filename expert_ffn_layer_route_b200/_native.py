@@ -34,6 +34,13 @@ class Weights(ctypes.Structure):
                 ("slot_map", ctypes.c_void_p), ("n_physical", ctypes.c_int32)]
 
 
+class GemmDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("n_physical", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("stride_w", ctypes.c_int64)]
+
+
 class WorkspaceLayout(ctypes.Structure):
     _fields_ = [("topk_idx", ctypes.c_size_t), ("topk_w", ctypes.c_size_t), ("offsets", ctypes.c_size_t),
                 ("row_token", ctypes.c_size_t), ("inv", ctypes.c_size_t), ("total", ctypes.c_size_t)]
@@ -63,6 +70,8 @@ _LIB = None
 _P = ctypes.c_void_p
 _DP = ctypes.POINTER(LayerDesc)
 _WP = ctypes.POINTER(Weights)
+_GP = ctypes.POINTER(GemmDesc)
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
 
 _SIGS = {
     "moe_workspace_size": [_DP, ctypes.POINTER(ctypes.c_size_t)],
@@ -73,6 +82,14 @@ _SIGS = {
     "moe_grouped_ffn": [_DP, _WP, _WP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_combine": [_DP, _P, _P, _P, _P, _P, _P],
     "moe_layer_forward": [_DP, _P, _P, _P, _WP, _WP, _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_gemm": [_GP, _P, _P, _P, _P, _P, _P],
+    "moe_grouped_gemm_grad_x": [_GP, _P, _P, _P, _P, _P, _P],
+    "moe_grouped_gemm_grad_w": [_GP, _P, _P, _P, _P, ctypes.c_int, _P],
+    "moe_grouped_gemm_i8": [_GP, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_quant_rows_i8": [_I32, _I32, _I32, _P, _I64, _P, _I32, _P, _I64, _P, _P],
+    "moe_swiglu": [_I32, _I32, _I32, _P, _I64, _P, _I64, _P],
+    "moe_swiglu_quant_i8": [_I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P],
+    "moe_swiglu_grad": [_I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P],
     "moe_cache_init": [ctypes.POINTER(_P), ctypes.POINTER(CacheDesc)],
     "moe_cache_prefetch": [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32],
     "moe_cache_lookup": [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32, _P, _P],
@@ -214,6 +231,249 @@ def moe_layer_forward(desc, x, w_router, logit_bias, routed: Weights, shared: Op
                                    ctypes.byref(routed), ctypes.byref(shared) if shared is not None else None,
                                    _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                    _stream(stream)), "moe_layer_forward")
+
+
+# ---------------------------------------------------------------------------
+# Expert operators.  These take whole tensors and read sizes, types and pitches
+# off them, so they also check them: the C entry points see only pointers.
+
+_DTYPE = {}  # torch dtype -> moe_dtype, filled on first use (torch is imported late)
+
+
+def _dtypes():
+    if not _DTYPE:
+        import torch
+
+        _DTYPE.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3})
+    return _DTYPE
+
+
+def _refuse(where: str, why: str):
+    raise MoeError(1, f"{where}: {why}")
+
+
+def _rows_of(t, rows, cols, where, name) -> int:
+    """Pitch of a [rows][cols] tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        _refuse(where, f"{name} has {t.dim()} dimensions, 2 are wanted")
+    if tuple(t.shape) != (rows, cols):
+        _refuse(where, f"{name} has shape {tuple(t.shape)}, ({rows}, {cols}) is wanted")
+    s = t.stride()
+    if s[1] != 1 and cols > 1:
+        _refuse(where, f"{name}'s rows are not contiguous")
+    return s[0] if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _matrices_of(t, E, N, K, where, name):
+    """(row pitch, distance of the matrices) of an [E][N][K] tensor."""
+    if t.dim() != 3 or t.shape[1] != N or t.shape[2] != K or (E is not None and t.shape[0] != E):
+        _refuse(where, f"{name} has shape {tuple(t.shape)}, ({'E' if E is None else E}, {N}, {K}) is wanted")
+    s = t.stride()
+    if s[2] != 1 and K > 1:
+        _refuse(where, f"{name}'s rows are not contiguous")
+    ld = s[1] if N > 1 else (K + 15) // 16 * 16
+    return ld, (s[0] if t.shape[0] > 1 else N * ld)
+
+
+def _vector(t, n, dtype, where, name):
+    if t.dim() != 1 or t.shape[0] < n or t.dtype != dtype or (t.shape[0] > 1 and t.stride(0) != 1):
+        _refuse(where, f"{name} has to be a contiguous {dtype} vector of at least {n} values")
+
+
+def _place(where, stream, *tensors):
+    """(device index, raw stream) of a call on these tensors, which have to lie on one GPU."""
+    import torch
+
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device != dev):
+            _refuse(where, "the tensors have to be on one CUDA device")
+    if stream is None:
+        return dev.index, torch._C._cuda_getCurrentRawStream(dev.index)
+    return dev.index, stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _launch(where, index, call, *args):
+    """call(*args) with device `index` current."""
+    import torch
+
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args)
+    if status != MOE_OK:
+        raise MoeError(status, where)
+
+
+def _groups(offsets, slot_map, E_w, where):
+    """Number of experts of a grouped product (E from offsets, checked against the matrices)."""
+    import torch
+
+    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != torch.int32 or offsets.stride(0) != 1:
+        _refuse(where, "offsets has to be a contiguous int32 vector of E + 1 values")
+    E = offsets.shape[0] - 1
+    if slot_map is not None:
+        _vector(slot_map, E, torch.int32, where, "slot_map")
+    elif E_w != E:
+        _refuse(where, f"{E_w} matrices for {E} experts (a slot_map would say which is whose)")
+    return E
+
+
+def moe_grouped_gemm(x, w, offsets, out, slot_map=None, stream=None):
+    """out[r] = x[r] w[e]^T for the rows r of each expert e (x [R][K], w [E][N][K], out [R][N])."""
+    where = "moe_grouped_gemm"
+    types = _dtypes()
+    if w.dim() != 3:
+        _refuse(where, "w has to be [E][N][K]")
+    Ew, N, K = w.shape
+    E = _groups(offsets, slot_map, Ew, where)
+    R = x.shape[0]
+    if x.dtype != w.dtype or types.get(x.dtype, 9) > 1 or types.get(out.dtype, 9) > 2:
+        _refuse(where, f"types {x.dtype}, {w.dtype} -> {out.dtype}")
+    ldx = _rows_of(x, R, K, where, "x")
+    ldy = _rows_of(out, R, N, where, "out")
+    ldw, sw = _matrices_of(w, None, N, K, where, "w")
+    d = GemmDesc(R, E, N, K, types[x.dtype], types[out.dtype], Ew, ldx, ldy, ldw, sw)
+    dev, st = _place(where, stream, x, w, offsets, out, slot_map)
+    _launch(where, dev, lib().moe_grouped_gemm, d, x.data_ptr(), w.data_ptr(), _ptr(slot_map), offsets.data_ptr(),
+            out.data_ptr(), st)
+
+
+def moe_grouped_gemm_grad_x(dy, w, offsets, dx, slot_map=None, stream=None):
+    """dx[r] = dy[r] w[e] for the rows r of each expert e (dy [R][N], w [E][N][K], dx [R][K])."""
+    where = "moe_grouped_gemm_grad_x"
+    types = _dtypes()
+    if w.dim() != 3:
+        _refuse(where, "w has to be [E][N][K]")
+    Ew, N, K = w.shape
+    E = _groups(offsets, slot_map, Ew, where)
+    R = dy.shape[0]
+    if dy.dtype != w.dtype or types.get(dy.dtype, 9) > 1 or types.get(dx.dtype, 9) > 2:
+        _refuse(where, f"types {dy.dtype}, {w.dtype} -> {dx.dtype}")
+    ldy = _rows_of(dy, R, N, where, "dy")
+    ldx = _rows_of(dx, R, K, where, "dx")
+    ldw, sw = _matrices_of(w, None, N, K, where, "w")
+    d = GemmDesc(R, E, N, K, types[dy.dtype], types[dx.dtype], Ew, ldx, ldy, ldw, sw)
+    dev, st = _place(where, stream, dy, w, offsets, dx, slot_map)
+    _launch(where, dev, lib().moe_grouped_gemm_grad_x, d, dy.data_ptr(), w.data_ptr(), _ptr(slot_map),
+            offsets.data_ptr(), dx.data_ptr(), st)
+
+
+def moe_grouped_gemm_grad_w(dy, x, offsets, dw, accumulate=False, stream=None):
+    """dw[e] (+)= dy[rows of e]^T x[rows of e] (dy [R][N], x [R][K], dw [E][N][K])."""
+    where = "moe_grouped_gemm_grad_w"
+    types = _dtypes()
+    if dw.dim() != 3:
+        _refuse(where, "dw has to be [E][N][K]")
+    E, N, K = dw.shape
+    _groups(offsets, None, E, where)
+    R = x.shape[0]
+    if x.dtype != dy.dtype or types.get(x.dtype, 9) > 1 or types.get(dw.dtype, 9) > 2:
+        _refuse(where, f"types {dy.dtype}, {x.dtype} -> {dw.dtype}")
+    ldx = _rows_of(x, R, K, where, "x")
+    ldy = _rows_of(dy, R, N, where, "dy")
+    ldw, sw = _matrices_of(dw, E, N, K, where, "dw")
+    d = GemmDesc(R, E, N, K, types[x.dtype], types[dw.dtype], 0, ldx, ldy, ldw, sw)
+    dev, st = _place(where, stream, dw, x, dy, offsets)
+    _launch(where, dev, lib().moe_grouped_gemm_grad_w, d, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(),
+            dw.data_ptr(), 1 if accumulate else 0, st)
+
+
+def moe_grouped_gemm_i8(x, x_scale, w, w_scale, offsets, out, slot_map=None, stream=None):
+    """out[r][n] = x_scale[r] w_scale[e][n] sum_k x[r][k] w[e][n][k] over int8 codes x [R][K], w [E][N][K]."""
+    import torch
+
+    where = "moe_grouped_gemm_i8"
+    types = _dtypes()
+    if w.dim() != 3:
+        _refuse(where, "w has to be [E][N][K]")
+    Ew, N, K = w.shape
+    E = _groups(offsets, slot_map, Ew, where)
+    R = x.shape[0]
+    if x.dtype != torch.int8 or w.dtype != torch.int8 or types.get(out.dtype, 9) > 2:
+        _refuse(where, f"types {x.dtype}, {w.dtype} -> {out.dtype}")
+    ldx = _rows_of(x, R, K, where, "x")
+    ldy = _rows_of(out, R, N, where, "out")
+    ldw, sw = _matrices_of(w, None, N, K, where, "w")
+    _vector(x_scale, R, torch.float32, where, "x_scale")
+    if tuple(w_scale.shape) != (Ew, N) or w_scale.dtype != torch.float32 or not w_scale.is_contiguous():
+        _refuse(where, f"w_scale has to be a contiguous float32 tensor of shape ({Ew}, {N})")
+    d = GemmDesc(R, E, N, K, 3, types[out.dtype], Ew, ldx, ldy, ldw, sw)
+    dev, st = _place(where, stream, x, x_scale, w, w_scale, offsets, out, slot_map)
+    _launch(where, dev, lib().moe_grouped_gemm_i8, d, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
+            w_scale.data_ptr(), _ptr(slot_map), offsets.data_ptr(), out.data_ptr(), st)
+
+
+def moe_quant_rows_i8(x, q, scale, row_token=None, stream=None):
+    """int8 codes q [R][K] and scale [R] of the rows of x, or of x[row_token[r]] (a dropped row: zeros)."""
+    import torch
+
+    where = "moe_quant_rows_i8"
+    types = _dtypes()
+    if x.dim() != 2 or q.dim() != 2:
+        _refuse(where, "x and q have to be matrices")
+    T, K = x.shape
+    R = q.shape[0]
+    if types.get(x.dtype, 9) > 1 or q.dtype != torch.int8:
+        _refuse(where, f"types {x.dtype} -> {q.dtype}")
+    if row_token is None:
+        if T != R:
+            _refuse(where, f"{T} rows of x, {R} of q")
+    else:
+        _vector(row_token, R, torch.int32, where, "row_token")
+    ldx = _rows_of(x, T, K, where, "x")
+    ldq = _rows_of(q, R, K, where, "q")
+    _vector(scale, R, torch.float32, where, "scale")
+    dev, st = _place(where, stream, x, q, scale, row_token)
+    _launch(where, dev, lib().moe_quant_rows_i8, R, K, types[x.dtype], x.data_ptr(), ldx, _ptr(row_token), T,
+            q.data_ptr(), ldq, scale.data_ptr(), st)
+
+
+def _gate_up(gate_up, where):
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2 or _dtypes().get(gate_up.dtype, 9) > 1:
+        _refuse(where, "gate_up has to be a bf16 or fp16 matrix [R][2F]")
+    R, F2 = gate_up.shape
+    return R, F2 // 2, _rows_of(gate_up, R, F2, where, "gate_up")
+
+
+def moe_swiglu(gate_up, h, stream=None):
+    """h = silu(gate_up[:, :F]) * gate_up[:, F:] (h [R][F])."""
+    where = "moe_swiglu"
+    R, F, ldg = _gate_up(gate_up, where)
+    if h.dtype != gate_up.dtype:
+        _refuse(where, f"types {gate_up.dtype} -> {h.dtype}")
+    ldh = _rows_of(h, R, F, where, "h")
+    dev, st = _place(where, stream, gate_up, h)
+    _launch(where, dev, lib().moe_swiglu, R, F, _DTYPE[h.dtype], gate_up.data_ptr(), ldg, h.data_ptr(), ldh, st)
+
+
+def moe_swiglu_quant_i8(gate_up, q, scale, stream=None):
+    """int8 codes q [R][F] and scale [R] of silu(gate_up[:, :F]) * gate_up[:, F:]."""
+    import torch
+
+    where = "moe_swiglu_quant_i8"
+    R, F, ldg = _gate_up(gate_up, where)
+    if q.dtype != torch.int8:
+        _refuse(where, f"types {gate_up.dtype} -> {q.dtype}")
+    ldq = _rows_of(q, R, F, where, "q")
+    _vector(scale, R, torch.float32, where, "scale")
+    dev, st = _place(where, stream, gate_up, q, scale)
+    _launch(where, dev, lib().moe_swiglu_quant_i8, R, F, _DTYPE[gate_up.dtype], gate_up.data_ptr(), ldg,
+            q.data_ptr(), ldq, scale.data_ptr(), st)
+
+
+def moe_swiglu_grad(gate_up, dh, dgate_up, stream=None):
+    """dgate_up [R][2F], the gradient of moe_swiglu at gate_up for a given dh [R][F]; it may be gate_up itself."""
+    where = "moe_swiglu_grad"
+    R, F, ldg = _gate_up(gate_up, where)
+    if dh.dtype != gate_up.dtype or dgate_up.dtype != gate_up.dtype:
+        _refuse(where, f"types {gate_up.dtype}, {dh.dtype} -> {dgate_up.dtype}")
+    ldh = _rows_of(dh, R, F, where, "dh")
+    ldd = _rows_of(dgate_up, R, 2 * F, where, "dgate_up")
+    dev, st = _place(where, stream, gate_up, dh, dgate_up)
+    _launch(where, dev, lib().moe_swiglu_grad, R, F, _DTYPE[dh.dtype], gate_up.data_ptr(), ldg, dh.data_ptr(), ldh,
+            dgate_up.data_ptr(), ldd, st)
 
 
 def moe_get_last_error() -> int:

@@ -15,6 +15,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "devinfo.cuh"
 #include "ffn_gemm_tc.cuh"
 
 namespace moe {
@@ -134,9 +135,9 @@ moe_status check_desc(const moe_layer_desc* d) {
   return MOE_OK;
 }
 
-struct DevInfo {
-  int sms = 0, smem_optin = 0, smem_per_sm = 0;
-};
+}  // namespace
+
+namespace moe {
 
 DevInfo dev_info() {
   static std::mutex mu;
@@ -152,6 +153,10 @@ DevInfo dev_info() {
   }
   return cache[dev];
 }
+
+}  // namespace moe
+
+namespace {
 
 moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 

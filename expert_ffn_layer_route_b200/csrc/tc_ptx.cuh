@@ -21,11 +21,32 @@ __device__ __forceinline__ uint64_t kmajor_sw128_desc(uint32_t smem_addr) {
          ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
+// Descriptor of a channel-major (M- or N-major) operand of 16-bit values: slabs
+// of 64 channels, each a column of 128-byte lines (one contraction row per
+// line, 128-byte swizzle, as a TMA box of 64 channels x rows writes them).
+// Leading byte offset = distance of the slabs, stride byte offset = 8 lines.
+__device__ __forceinline__ uint64_t mnmajor_sw128_desc(uint32_t smem_addr, uint32_t slab_bytes) {
+  return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)(slab_bytes >> 4) << 16) |
+         ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
 // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B bf16
 // (bits 7-9 and 10-12 = 1), both K-major (bits 15, 16 = 0), N >> 3 in bits
 // 17-22, M >> 4 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same without N (added per tile, N >> 3 in bits 17-22): bf16 or fp16
+// operands, either one channel-major (bit 15: A, bit 16: B).
+__host__ __device__ constexpr uint32_t idesc_16_f32(int M, bool bf16, bool a_chan_major, bool b_chan_major) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_chan_major ? 1u << 15 : 0u) |
+         (b_chan_major ? 1u << 16 : 0u) | ((uint32_t)(M >> 4) << 24);
+}
+// kind::i8, without N: D int32 (bits 4-5 = 2), A and B signed (bits 7-9 and
+// 10-12 = 1), both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8_s32(int M) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(M >> 4) << 24);
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* smem_dst, uint32_t ncols) {
@@ -49,6 +70,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T in 8-bit integers, one instruction (K = 32).
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

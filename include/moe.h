@@ -224,6 +224,106 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, const vo
                              size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Expert operators: the parts of the expert FFN as calls of their own, for
+ * programs that compose the layer themselves - train it, or serve 8-bit
+ * integer experts.  Not part of the pages' method (the pages describe
+ * inference over bf16 and 4-bit experts).
+ *
+ * A grouped product multiplies the activation rows [offsets[e], offsets[e+1])
+ * of each expert e by that expert's matrix; offsets, and the order of the
+ * rows, are what moe_permute writes.  Offsets have to be non-decreasing and
+ * within [0, rows]; a pair that is not sets MOE_ERR_DEVICE_INDEX and counts as
+ * an empty group.  Rows in no group (before offsets[0], behind offsets[E]),
+ * and the rows of an expert that slot_map calls not resident (-1), are neither
+ * read into any result nor written.
+ *
+ * Values of each product are exact products summed in fp32 (int8: exactly, in
+ * int32) and rounded once to the output type.  The result of a row depends on
+ * no other row, and the same call gives the same bits again.  Groups may be
+ * empty, of one row, or all rows; nothing has to be a multiple of anything,
+ * but the matrices that are read (w, x, dy, codes) need a base and a row pitch
+ * of whole 16 bytes.  Outputs need only the alignment of their type; pitches
+ * of whole 16 bytes are stored faster.
+ * No call needs a workspace; none allocates.  All may be captured into a
+ * CUDA graph.  Outputs must not overlap inputs unless a call says so.
+ * ---------------------------------------------------------------------- */
+typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2, MOE_T_INT8 = 3 } moe_dtype;
+
+typedef struct {
+  int32_t rows;        /* rows the activation buffers hold (>= offsets[E]) */
+  int32_t n_experts;   /* E <= 1024 */
+  int32_t N, K;        /* an expert's matrix is [N][K]; 1 <= N, K <= 2^20 (int8: K <= 131071) */
+  int32_t dtype;       /* moe_dtype of the operands: bf16 or fp16 (moe_grouped_gemm_i8: int8) */
+  int32_t out_dtype;   /* moe_dtype of the result: bf16, fp16 or fp32 */
+  int32_t n_physical;  /* matrices that w holds (0: n_experts) */
+  int64_t ld_x;        /* row pitch of x, codes, dx [rows][K] in elements (0: K) */
+  int64_t ld_y;        /* row pitch of out, dy [rows][N] in elements (0: N) */
+  int64_t ld_w;        /* row pitch of w, dw [N][K] in elements (0: K) */
+  int64_t stride_w;    /* elements between experts' matrices in w, dw (0: N * ld_w) */
+} moe_gemm_desc;
+
+/* out[r][n] = sum_k x[r][k] * w[p][n][k], p = slot_map ? slot_map[e] : e.
+ * x [rows][K], w [n_physical][N][K], out [rows][N].  slot_map: device int32
+ * [E] or NULL; an entry of -1 skips the expert, any other entry outside
+ * [0, n_physical) also sets MOE_ERR_DEVICE_INDEX. */
+moe_status moe_grouped_gemm(const moe_gemm_desc* desc, const void* x, const void* w, const int32_t* slot_map,
+                            const int32_t* offsets, void* out, void* stream);
+
+/* Gradient of moe_grouped_gemm with respect to x:
+ * dx[r][k] = sum_n dy[r][n] * w[p][n][k].  out_dtype is dx's. */
+moe_status moe_grouped_gemm_grad_x(const moe_gemm_desc* desc, const void* dy, const void* w,
+                                   const int32_t* slot_map, const int32_t* offsets, void* dx, void* stream);
+
+/* Gradient of moe_grouped_gemm with respect to w:
+ * dw[e][n][k] = sum_{r of e} dy[r][n] * x[r][k], zeros for an expert without
+ * rows; with accumulate != 0 (fp32 only) the sum is added to what dw holds,
+ * rounded once.  out_dtype is dw's.  rows = 0 is a call like any other (it
+ * writes zeros). */
+moe_status moe_grouped_gemm_grad_w(const moe_gemm_desc* desc, const void* dy, const void* x,
+                                   const int32_t* offsets, void* dw, int accumulate, void* stream);
+
+/* out[r][n] = x_scale[r] * w_scale[p][n] * sum_k x[r][k] * w[p][n][k] in 8-bit
+ * integers: the sum is exact (int32), then times the fp32 product of the two
+ * scales.  x: int8 codes [rows][K], x_scale fp32 [rows]; w: int8 codes
+ * [n_physical][N][K], w_scale fp32 [n_physical][N].  E = 1 with offsets
+ * {0, rows} is the plain product. */
+moe_status moe_grouped_gemm_i8(const moe_gemm_desc* desc, const int8_t* x, const float* x_scale, const int8_t* w,
+                               const float* w_scale, const int32_t* slot_map, const int32_t* offsets, void* out,
+                               void* stream);
+
+/* 8-bit rows: with v = x[row_token ? row_token[r] : r], amax = max|v|,
+ *   scale[r] = amax / 127,  q[r][k] = round(v[k] * (127 / amax)),
+ * both quotients and the product rounded to fp32, the code to the nearest
+ * integer, ties to even.  A row whose amax is below 2^-120 becomes zeros with
+ * scale 0, as does a row whose row_token lies outside [0, n_tokens) (a pair
+ * that moe_permute dropped).  A row that holds a NaN or an infinity becomes
+ * zeros with scale NaN, so that every product with it is NaN.
+ * x: bf16 or fp16 (dtype) [n_tokens][K] of pitch ld_x; q int8 [rows][K] of
+ * pitch ld_q; scale fp32 [rows]; pitches in elements, 0: K.  row_token: device
+ * int32 [rows], or NULL (n_tokens is then not looked at). */
+moe_status moe_quant_rows_i8(int32_t rows, int32_t K, int32_t dtype, const void* x, int64_t ld_x,
+                             const int32_t* row_token, int32_t n_tokens, int8_t* q, int64_t ld_q, float* scale,
+                             void* stream);
+
+/* h[r][f] = silu(g) * u, g = gate_up[r][f], u = gate_up[r][F + f] (the order
+ * of W13's rows), computed in fp32.  gate_up [rows][2F] of pitch ld_gu (0: 2F),
+ * h [rows][F] of pitch ld_h (0: F), both bf16 or fp16. */
+moe_status moe_swiglu(int32_t rows, int32_t F, int32_t dtype, const void* gate_up, int64_t ld_gu, void* h,
+                      int64_t ld_h, void* stream);
+
+/* moe_swiglu straight into 8-bit rows (the rule of moe_quant_rows_i8 on the
+ * fp32 values of h): what the int8 down projection reads. */
+moe_status moe_swiglu_quant_i8(int32_t rows, int32_t F, int32_t dtype, const void* gate_up, int64_t ld_gu,
+                               int8_t* q, int64_t ld_q, float* scale, void* stream);
+
+/* Gradient of moe_swiglu: with s = 1 / (1 + e^-g),
+ *   dgate_up[r][f] = dh u s (1 + g (1 - s)),  dgate_up[r][F + f] = dh g s.
+ * dh [rows][F] of pitch ld_h, dgate_up [rows][2F] of pitch ld_d (0: 2F), which
+ * may be gate_up itself (same base and pitch). */
+moe_status moe_swiglu_grad(int32_t rows, int32_t F, int32_t dtype, const void* gate_up, int64_t ld_gu,
+                           const void* dh, int64_t ld_h, void* dgate_up, int64_t ld_d, void* stream);
+
+/* ------------------------------------------------------------------------
  * Expert cache: per-layer LRU over HBM slots, filled from a pinned host bank.
  * Policy (per layer, `slots_per_layer` slots): lookup walks its experts in
  * ascending id, in waves of at most slots_per_layer; a resident expert (copied

@@ -1,0 +1,181 @@
+"""Refusals of the expert operators, answered on the host before anything is
+enqueued: no GPU needed, and no pointer is followed."""
+import ctypes
+
+import pytest
+import torch
+
+import expert_ffn_layer_route_b200 as moe
+
+INVALID, UNSUPPORTED = 1, 2
+P = 4096  # a 16-byte aligned address that nothing follows
+
+
+def _desc(**kw):
+    d = dict(rows=4, n_experts=2, N=32, K=48, dtype=0, out_dtype=0, n_physical=0, ld_x=0, ld_y=0, ld_w=0, stride_w=0)
+    d.update(kw)
+    return moe.GemmDesc(*[d[f] for f, _ in moe.GemmDesc._fields_])
+
+
+def _forward(d, x=P, w=P, off=P, out=P):
+    return moe.lib().moe_grouped_gemm(ctypes.byref(d), x, w, None, off, out, None)
+
+
+def _grad_x(d, dy=P, w=P, off=P, dx=P):
+    return moe.lib().moe_grouped_gemm_grad_x(ctypes.byref(d), dy, w, None, off, dx, None)
+
+
+def _grad_w(d, dy=P, x=P, off=P, dw=P, acc=0):
+    return moe.lib().moe_grouped_gemm_grad_w(ctypes.byref(d), dy, x, off, dw, acc, None)
+
+
+def _int8(d, x=P, sx=P, w=P, sw=P, off=P, out=P):
+    return moe.lib().moe_grouped_gemm_i8(ctypes.byref(d), x, sx, w, sw, None, off, out, None)
+
+
+BAD = [
+    (dict(rows=-1), INVALID), (dict(n_experts=0), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID),
+    (dict(n_physical=-1), INVALID), (dict(out_dtype=3), INVALID), (dict(out_dtype=-1), INVALID),
+    (dict(ld_x=47), INVALID), (dict(ld_y=31), INVALID), (dict(ld_w=47), INVALID), (dict(stride_w=31 * 48 + 47), INVALID),
+    (dict(n_experts=1025), UNSUPPORTED), (dict(N=(1 << 20) + 1), UNSUPPORTED), (dict(K=(1 << 20) + 1), UNSUPPORTED),
+    (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(ld_w=1 << 31), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD, ids=[str(b[0]) for b in BAD])
+def test_bad_descriptions(kw, status):
+    assert _forward(_desc(**kw)) == status
+    assert _grad_x(_desc(**kw)) == status
+    assert _grad_w(_desc(**kw)) == status
+    assert _int8(_desc(dtype=3, **kw)) == status
+
+
+def test_types():
+    for dtype in (2, 3, 4, -1):
+        assert _forward(_desc(dtype=dtype)) == INVALID
+        assert _grad_x(_desc(dtype=dtype)) == INVALID
+        assert _grad_w(_desc(dtype=dtype)) == INVALID
+    for dtype in (0, 1, 2):
+        assert _int8(_desc(dtype=dtype)) == INVALID
+    assert _int8(_desc(dtype=3, K=131072)) == UNSUPPORTED  # the int32 sum could overflow
+    for out in (0, 1):
+        assert _grad_w(_desc(out_dtype=out), acc=1) == INVALID  # sums are accumulated in fp32 only
+
+
+def test_null_and_misaligned():
+    d, q = _desc(), _desc(dtype=3)
+    L = moe.lib()
+    assert L.moe_grouped_gemm(None, P, P, None, P, P, None) == INVALID
+    for bad in (None, P + 8):  # matrices that are read lie on 16 bytes
+        assert _forward(d, x=bad) == _forward(d, w=bad) == INVALID
+        assert _grad_x(d, dy=bad) == _grad_x(d, w=bad) == INVALID
+        assert _grad_w(d, dy=bad) == _grad_w(d, x=bad) == INVALID
+        assert _int8(q, x=bad) == _int8(q, w=bad) == INVALID
+    for bad in (None, P + 1):  # results on their type
+        assert _forward(d, out=bad) == _grad_x(d, dx=bad) == _grad_w(d, dw=bad) == _int8(q, out=bad) == INVALID
+    assert _forward(_desc(out_dtype=2), out=P + 2) == INVALID
+    assert _int8(q, sx=None) == _int8(q, sw=None) == _int8(q, sx=P + 2) == INVALID
+    assert _forward(d, off=None) == _grad_x(d, off=None) == _grad_w(d, off=None) == _int8(q, off=None) == INVALID
+    # row pitches of what is read: whole 16 bytes
+    assert _forward(_desc(ld_x=52)) == _forward(_desc(ld_w=52)) == _forward(_desc(K=50)) == INVALID
+    assert _grad_x(_desc(ld_y=36)) == _grad_x(_desc(ld_w=52)) == INVALID
+    assert _grad_w(_desc(ld_y=36)) == _grad_w(_desc(ld_x=52)) == INVALID
+    assert _int8(_desc(dtype=3, ld_x=56)) == _int8(_desc(dtype=3, ld_w=56)) == INVALID
+    assert _forward(_desc(stride_w=32 * 48 + 4)) == INVALID
+
+
+def test_no_rows_is_a_no_op():
+    z = _desc(rows=0)
+    assert _forward(z, None, None, None, None) == 0
+    assert _grad_x(z, None, None, None, None) == 0
+    assert _int8(_desc(rows=0, dtype=3), None, None, None, None, None, None) == 0
+    assert _grad_w(z, None, None, None, None) == INVALID  # it has zeros to write
+    L = moe.lib()
+    assert L.moe_quant_rows_i8(0, 8, 0, None, 0, None, 0, None, 0, None, None) == 0
+    assert L.moe_swiglu(0, 8, 0, None, 0, None, 0, None) == 0
+    assert L.moe_swiglu_quant_i8(0, 8, 0, None, 0, None, 0, None, None) == 0
+    assert L.moe_swiglu_grad(0, 8, 0, None, 0, None, 0, None, 0, None) == 0
+
+
+def test_row_operators():
+    L = moe.lib()
+
+    def quant(rows=4, K=8, t=0, x=P, ldx=0, tok=None, n=4, q=P, ldq=0, s=P):
+        return L.moe_quant_rows_i8(rows, K, t, x, ldx, tok, n, q, ldq, s, None)
+
+    def swiglu(rows=4, F=8, t=0, gu=P, ldg=0, h=P, ldh=0):
+        return L.moe_swiglu(rows, F, t, gu, ldg, h, ldh, None)
+
+    def swiglu_q(rows=4, F=8, t=0, gu=P, ldg=0, q=P, ldq=0, s=P):
+        return L.moe_swiglu_quant_i8(rows, F, t, gu, ldg, q, ldq, s, None)
+
+    def grad(rows=4, F=8, t=0, gu=P, ldg=0, dh=P, ldh=0, d=2 * P, ldd=0):
+        return L.moe_swiglu_grad(rows, F, t, gu, ldg, dh, ldh, d, ldd, None)
+
+    for f, width in ((quant, "K"), (swiglu, "F"), (swiglu_q, "F"), (grad, "F")):
+        assert f(rows=-1) == f(**{width: 0}) == f(t=2) == f(t=3) == f(t=-1) == INVALID
+        assert f(**{width: (1 << 20) + 1}) == f(rows=(1 << 30) + 1) == UNSUPPORTED
+        assert f(rows=1 << 30, **{width: 1 << 20}) == UNSUPPORTED
+    assert quant(x=None) == quant(x=P + 1) == quant(q=None) == quant(s=None) == quant(s=P + 2) == INVALID
+    assert quant(ldx=7) == quant(ldq=7) == quant(tok=P, n=-1) == quant(tok=P + 2) == INVALID
+    assert swiglu(gu=None) == swiglu(gu=P + 1) == swiglu(h=None) == swiglu(ldg=15) == swiglu(ldh=7) == INVALID
+    assert swiglu_q(gu=None) == swiglu_q(q=None) == swiglu_q(s=None) == swiglu_q(ldg=15) == swiglu_q(ldq=7) == INVALID
+    assert grad(gu=None) == grad(dh=None) == grad(d=None) == grad(ldg=15) == grad(ldh=7) == grad(ldd=15) == INVALID
+    assert grad(d=P, ldd=24) == INVALID  # in place with another pitch
+
+
+# ---- the Python calls check the tensors they are given
+
+def _t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _refused(f, *a, **k):
+    with pytest.raises(moe.MoeError) as e:
+        f(*a, **k)
+    assert e.value.status == INVALID
+    return str(e.value)
+
+
+def test_python_calls_check_shapes_types_and_places():
+    x, w, off, out = _t(4, 16), _t(2, 8, 16), torch.zeros(3, dtype=torch.int32), _t(4, 8)
+    f = moe.moe_grouped_gemm
+    assert "CUDA" in _refused(f, x, w, off, out)  # host tensors
+    assert "shape" in _refused(f, x, w, off, _t(4, 9))
+    assert "shape" in _refused(f, _t(4, 15), w, off, out)
+    assert "shape" in _refused(f, x, w, off, _t(5, 8))
+    assert "types" in _refused(f, x.half(), w, off, out)
+    assert "types" in _refused(f, x.float(), w.float(), off, out)
+    assert "types" in _refused(f, x, w, off, out.double())
+    assert "offsets" in _refused(f, x, w, off.long(), out)
+    assert "offsets" in _refused(f, x, w, off[:1], out)
+    assert "matrices" in _refused(f, x, w, torch.zeros(4, dtype=torch.int32), out)
+    assert "slot_map" in _refused(f, x, w, torch.zeros(4, dtype=torch.int32), out, slot_map=off[:2])
+    assert "contiguous" in _refused(f, _t(16, 4).t(), w, off, out)
+    assert "contiguous" in _refused(f, x, _t(2, 16, 8).transpose(1, 2), off, out)
+    assert "CUDA" in _refused(moe.moe_grouped_gemm_grad_x, out, w, off, x)
+    assert "shape" in _refused(moe.moe_grouped_gemm_grad_x, out, w, off, _t(4, 8))
+    assert "CUDA" in _refused(moe.moe_grouped_gemm_grad_w, out, x, off, w)
+    assert "shape" in _refused(moe.moe_grouped_gemm_grad_w, out, _t(5, 16), off, w)
+    assert "matrices" in _refused(moe.moe_grouped_gemm_grad_w, out, x, off, _t(3, 8, 16))
+    xq, wq = _t(4, 16, dtype=torch.int8), _t(2, 8, 16, dtype=torch.int8)
+    sx, sw = torch.zeros(4), torch.zeros(2, 8)
+    g = moe.moe_grouped_gemm_i8
+    assert "CUDA" in _refused(g, xq, sx, wq, sw, off, out)
+    assert "types" in _refused(g, x, sx, wq, sw, off, out)
+    assert "x_scale" in _refused(g, xq, sx[:3], wq, sw, off, out)
+    assert "x_scale" in _refused(g, xq, sx.double(), wq, sw, off, out)
+    assert "w_scale" in _refused(g, xq, sx, wq, sw[:, :7], off, out)
+    q = moe.moe_quant_rows_i8
+    assert "CUDA" in _refused(q, x, xq, sx)
+    assert "rows" in _refused(q, _t(3, 16), xq, sx)
+    assert "row_token" in _refused(q, _t(3, 16), xq, sx, row_token=off)
+    assert "types" in _refused(q, x.float(), xq, sx)
+    gu = _t(4, 32)
+    assert "CUDA" in _refused(moe.moe_swiglu, gu, x)
+    assert "types" in _refused(moe.moe_swiglu, gu, x.half())
+    assert "gate_up" in _refused(moe.moe_swiglu, _t(4, 31), x)
+    assert "CUDA" in _refused(moe.moe_swiglu_quant_i8, gu, xq, sx)
+    assert "scale" in _refused(moe.moe_swiglu_quant_i8, gu, xq, sx[:2])
+    assert "CUDA" in _refused(moe.moe_swiglu_grad, gu, x, gu)
+    assert "shape" in _refused(moe.moe_swiglu_grad, gu, x, _t(4, 30))
