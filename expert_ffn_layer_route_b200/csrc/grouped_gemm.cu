@@ -27,18 +27,24 @@ namespace moe {
 
 namespace {
 
-constexpr int kChan = 128;             // channels per tile = TMEM lanes
-constexpr int kStageK = 128;           // bytes of the contraction per stage (one swizzle line)
-constexpr int kABytes = kChan * kStageK;
-constexpr int kSlabBytes = 64 * 128;   // 64 contraction rows x 64 channels of 16 bits
+constexpr int kLine = 128;             // bytes of the contraction per K-major block (one swizzle line)
+constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction rows x 64 channels of 16 bits
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 4;
-constexpr int kEpiBytes = 2560;        // transposition buffer of one epilogue warp
 constexpr int kGgThreads = 32 * (2 + kEpiWarps);
+constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of the ragged operand
+
+// Staging buffer of one epilogue warp: 32 rows x 32 channels (forward, grad_x,
+// int8; rows padded against bank conflicts), or two 32-row blocks of 128-byte
+// swizzled lines that TMA stores read (grad_w).
+constexpr int kPitch16 = 80, kPitch32 = 144;
+constexpr int epi_bytes(int kind) { return kind == kGgGradW ? 2 * 32 * 128 : 5 * 1024; }
 
 struct alignas(64) GgArgs {
   CUtensorMap tm_a;
-  CUtensorMap tm_b;
+  CUtensorMap tm_b;    // 64-row boxes
+  CUtensorMap tm_b16;  // 16-row boxes
+  CUtensorMap tm_o;    // grad_w's result
   const int32_t* offsets;
   const int32_t* slot_map;
   const float* x_scale;
@@ -47,14 +53,17 @@ struct alignas(64) GgArgs {
   int64_t ldo, stride_o;
   int E, rows, n_phys;
   int channels;  // M extent: N (forward, grad_w, int8) or K (grad_x)
-  int depth;     // contraction extent in elements (grad_w: unused)
+  int depth;     // contraction extent in elements (grad_w: the group's rows)
   int cols;      // grad_w: K
+  int tile_m;    // channels per CTA and tile (TMEM lanes in use)
   int col_cap;   // widest column tile
-  int box_rows;  // rows of one TMA box of B (K-major kinds)
-  int stages, stage_bytes, tmem_cols;
+  int col_step;  // column tiles start on multiples of this
+  int blocks;    // 128-byte contraction blocks per stage
+  int stages, a_block, b_block, stage_bytes, tmem_cols;
   uint32_t idesc;  // instruction descriptor without N
   int out_dtype;
-  int vec_ok;  // output rows start on 16-byte boundaries
+  int vec;        // widest store the result's address and pitches allow (bytes)
+  int tma_out;    // grad_w: tm_o is in use
   int accumulate;
 };
 
@@ -66,21 +75,12 @@ struct Group {
 };
 
 struct Tile {
-  int m0;            // first channel
+  int m0;            // first channel (of the pair)
   int c0, nc;        // first column (row inside the group; grad_w: k) and columns that exist
-  int ncols;         // MMA N: nc rounded up to 16
+  int ncols;         // MMA N: nc rounded up
   int row0, n;       // the group's rows
   int expert, phys;
 };
-
-__device__ __forceinline__ void store_one(void* out, int dtype, int64_t i, float v) {
-  if (dtype == MOE_T_FP32)
-    static_cast<float*>(out)[i] = v;
-  else if (dtype == MOE_T_BF16)
-    static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(out)[i] = __float2half_rn(v);
-}
 
 __device__ __forceinline__ uint32_t pack16(int dtype, float lo, float hi) {
   if (dtype == MOE_T_BF16) {
@@ -96,35 +96,72 @@ __device__ __forceinline__ uint32_t pack16(int dtype, float lo, float hi) {
 // cleared in both operands, so that neither their values nor a NaN among them
 // reaches the sum.  A contraction row is one 128-byte line of each 64-channel
 // slab, whatever the swizzle.
-__device__ __forceinline__ void clear_tail(uint8_t* stage, int left, int ncols, int lane) {
+__device__ __forceinline__ void clear_tail(uint8_t* block, int left, int slabs, int lane) {
   const int per_slab = (16 - (left & 15)) * 8;  // 16-byte pieces
-  const int slabs = 2 + ceil_div(ncols, 64);
   for (int i = lane; i < slabs * per_slab; i += 32) {
     const int sl = i / per_slab, w = i - sl * per_slab;
-    reinterpret_cast<uint4*>(stage + sl * kSlabBytes + left * 128)[w] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(block + sl * kSlabBytes + left * 128)[w] = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   __syncwarp();
 }
 
+// One row's staged bytes to global memory in pieces of `vec` bytes, the pieces
+// of 32 lanes side by side; rows [0, n), bytes [0, width) of each.
+template <int kVec>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const uint8_t* staged, int staged_pitch,
+                                           int row_bytes, int n, int width, int elem, int lane) {
+  const int shift = 31 - __clz(row_bytes / kVec);
+  for (int i = lane; i < (n << shift); i += 32) {
+    const int j = i >> shift, b = (i - (j << shift)) * kVec;
+    uint8_t* d = out + j * pitch + b;
+    const uint8_t* s = staged + j * staged_pitch + b;
+    if (b + kVec <= width) {
+      if constexpr (kVec == 16) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+      if constexpr (kVec == 8) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
+      if constexpr (kVec == 4) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
+      if constexpr (kVec == 2) *reinterpret_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(s);
+    } else {
+      for (int z = 0; b + z < width; z += elem) {
+        if (elem == 4)
+          *reinterpret_cast<uint32_t*>(d + z) = *reinterpret_cast<const uint32_t*>(s + z);
+        else
+          *reinterpret_cast<uint16_t*>(d + z) = *reinterpret_cast<const uint16_t*>(s + z);
+      }
+    }
+  }
+}
+
 }  // namespace
 
-template <int kKind>
+// kPair: two CTAs (a cluster, on neighbouring SMs) share one tile of 256
+// channels: each loads its 128 channels of A and half of the columns of B, the
+// even CTA issues one MMA for both, and each keeps its 128 channels of D.  Each
+// operand byte then crosses L2 -> SM half as often as with tiles of one CTA.
+template <int kKind, bool kPair>
 __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __grid_constant__ GgArgs a) {
   constexpr bool kAChanMajor = kKind == kGgGradX || kKind == kGgGradW;  // A rows run along the channels
   constexpr bool kBChanMajor = kKind == kGgGradW;
   constexpr int kElem = kKind == kGgInt8 ? 1 : 2;
-  constexpr int kDepthStage = kAChanMajor ? 64 : kStageK / kElem;  // contraction elements per stage
-  constexpr int kDepthMma = kKind == kGgInt8 ? 32 : 16;
+  constexpr int kDepthBlock = kLine / kElem;  // contraction elements per block
+  constexpr int kDepthMma = 32 / kElem;
+  constexpr int kColRound = kPair ? 32 : 16;
+  constexpr int kEpiBytes = epi_bytes(kKind);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, for the compiler too
+  const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
+  const int unit = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int units = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
   uint8_t* epi = ring + (size_t)a.stages * a.stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(epi + kEpiWarps * kEpiBytes);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* tail = empty + kMaxStages;  // grad_w: this CTA's half of a group's last stage has landed
+  uint64_t* peer = tail + kMaxStages;   // grad_w: the odd CTA has cleared its half of it
+  uint64_t* acc_full = peer + kMaxStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -136,19 +173,18 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&tail[i], 1);
+      mbar_init(&peer[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpiWarps);
+      mbar_init(&acc_empty[i], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == 1) {
-    tc::tmem_alloc(s_tmem, a.tmem_cols);
-    tc::tmem_relinquish();
-  }
+  if (warp == 1) tc::tmem_alloc_g<kPair>(s_tmem, a.tmem_cols);
   pdl_wait_and_trigger();
   // Group table.  Every thread loads the offsets of some experts (one round of
   // global latency for all of them), then warp 0 compacts and numbers them.
@@ -171,8 +207,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     grp[e].phys = p;
   }
   __syncthreads();
-  const int m_tiles = ceil_div(a.channels, kChan);
   if (warp == 0) {
+    const int m_tiles = ceil_div(a.channels, kPair ? 2 * a.tile_m : a.tile_m);
     int ng = 0, tiles = 0;
     for (int base = 0; base < a.E; base += 32) {
       const int e = base + lane;
@@ -181,7 +217,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
         row0 = grp[e].row0;
         n = grp[e].n;
         p = grp[e].phys;
-        t = m_tiles * (kKind == kGgGradW ? ceil_div(a.cols, a.col_cap) : ceil_div(n, a.col_cap));
+        if (kKind == kGgGradW)  // a group without rows has zeros to write, unless they would be added
+          t = n == 0 && a.accumulate ? 0 : m_tiles * ceil_div(a.cols, a.col_cap);
+        else
+          t = m_tiles * ceil_div(n, a.col_cap);
       }
       const uint32_t on = __ballot_sync(0xffffffffu, t > 0);
       int incl = t;
@@ -210,10 +249,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   }
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (kPair) cluster_sync_all();  // the peer's barriers are initialised
   tc::fence_after_sync();
-  const uint32_t tmem_base = *s_tmem;
-  const int ngroups = *s_ngroups;
-  const int total_tiles = grp[ngroups].tile0;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *s_tmem, 0);
+  const int ngroups = __shfl_sync(0xffffffffu, *s_ngroups, 0);
+  const int total_tiles = __shfl_sync(0xffffffffu, grp[ngroups].tile0, 0);
 
   auto decode = [&](int t) {
     int lo = 0, hi = ngroups - 1;
@@ -229,110 +269,190 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     ti.phys = g.phys;
     const int local = t - g.tile0;
     const int width = kKind == kGgGradW ? a.cols : g.n;
-    const int ct = ceil_div(width, a.col_cap);                 // column tiles, as even as 16 allows
-    const int w = (ceil_div(width, ct) + 15) & ~15;
-    const int mi = local / ct;                                  // column tiles of one channel tile run side by side
-    ti.m0 = mi * kChan;
+    const int ct = ceil_div(width, a.col_cap);  // column tiles, as even as their step allows
+    const int w = ceil_div(ceil_div(width, ct), a.col_step) * a.col_step;
+    const int mi = local / ct;                  // column tiles of one channel tile run side by side
+    ti.m0 = mi * (kPair ? 2 * a.tile_m : a.tile_m);
     ti.c0 = (local - mi * ct) * w;
     ti.nc = min(w, width - ti.c0);
-    ti.ncols = (ti.nc + 15) & ~15;
+    ti.ncols = (ti.nc + kColRound - 1) & ~(kColRound - 1);
     return ti;
   };
-  auto steps_of = [&](const Tile& ti) {
-    return ceil_div(kKind == kGgGradW ? ti.n : a.depth, kDepthStage);
-  };
+  const int step_depth = kDepthBlock * a.blocks;
+  auto depth_of = [&](const Tile& ti) { return kKind == kGgGradW ? ti.n : a.depth; };
+  // grad_w: whether a step ends inside a group of 16 contraction rows
+  auto ragged = [&](int left) { return kKind == kGgGradW && left < kDepthBlock && (left & 15) != 0; };
 
   if (warp == 0) {
     // ================================================================ TMA producer
-    if (lane == 0) {
-      if (a.rows > 0) {
-        prefetch_tmap(&a.tm_a);
-        prefetch_tmap(&a.tm_b);
-      }
-      const uint64_t pol = l2_evict_normal_policy();
-      uint32_t s = 0, par = 1, cnt = 0;
-      for (int t = blockIdx.x; t < total_tiles && !*s_abort; t += gridDim.x) {
-        const Tile ti = decode(t);
-        const int steps = steps_of(ti);
-        const int boxes = kBChanMajor ? ceil_div(ti.ncols, 64) : ceil_div(ti.ncols, a.box_rows);
-        const uint32_t bytes = kABytes + boxes * (kBChanMajor ? kSlabBytes : a.box_rows * kStageK);
-        for (int ks = 0; ks < steps; ++ks) {
-          if (!mbar_wait(&empty[s], par)) {
-            *s_abort = 1;
-            break;
-          }
-          uint8_t* sa = ring + (size_t)s * a.stage_bytes;
-          uint8_t* sb = sa + kABytes;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          if (kKind == kGgGradW) {
-            const int r = ti.row0 + ks * 64;
-            for (int i = 0; i < 2; ++i)
-              tma_load_2d(sa + i * kSlabBytes, &a.tm_a, (ti.m0 + 64 * i) * 2, r, &full[s], pol);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(sb + i * kSlabBytes, &a.tm_b, (ti.c0 + 64 * i) * 2, r, &full[s], pol);
-          } else {
-            if (kKind == kGgGradX) {
-              for (int i = 0; i < 2; ++i)
-                tma_load_3d(sa + i * kSlabBytes, &a.tm_a, (ti.m0 + 64 * i) * 2, ks * 64, ti.phys, &full[s], pol);
-            } else {
-              tma_load_3d(sa, &a.tm_a, ks * kStageK, ti.m0, ti.phys, &full[s], pol);
-            }
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(sb + i * a.box_rows * kStageK, &a.tm_b, ks * kStageK,
-                          ti.row0 + ti.c0 + i * a.box_rows, &full[s], pol);
-          }
-          ++cnt;
-          if (++s == (uint32_t)a.stages) {
-            s = 0;
-            par ^= 1;
-          }
-        }
-      }
-      // every copy has landed before the block may leave
-      const uint32_t first = cnt > (uint32_t)a.stages ? cnt - a.stages : 0;
-      for (uint32_t c = first; c < cnt; ++c) mbar_wait(&full[c % a.stages], (c / a.stages) & 1u);
+    // (the whole warp runs the loops, one lane is elected to issue: see the MMA warp)
+    if (a.rows > 0 && tc::elect_one()) {
+      prefetch_tmap(&a.tm_a);
+      prefetch_tmap(&a.tm_b);
+      if (!kBChanMajor) prefetch_tmap(&a.tm_b16);
     }
-  } else if (warp == 1) {
-    // ================================================================ MMA issuer
-    // (the whole warp follows the ring; lane 0 issues)
-    uint32_t s = 0, par = 0;
-    int i = 0;
-    for (int t = blockIdx.x; t < total_tiles; t += gridDim.x, ++i) {
+    const uint64_t pol = l2_evict_normal_policy();
+    uint32_t s = 0, par = 1, cnt = 0, tails = 0, tail_use = 0;
+    for (int t = unit; t < total_tiles; t += units) {
+      if (*s_abort) break;
       const Tile ti = decode(t);
-      const int buf = i & 1;
-      if (*s_abort || !mbar_wait(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
-        *s_abort = 1;
-        break;
-      }
-      tc::fence_after_sync();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * a.col_cap);
-      const uint32_t idesc = a.idesc | ((uint32_t)(ti.ncols >> 3) << 17);
-      const int steps = steps_of(ti);
-      const int depth = kKind == kGgGradW ? ti.n : a.depth;
-      for (int ks = 0; ks < steps; ++ks) {
-        if (!mbar_wait(&full[s], par)) {
+      const int depth = __shfl_sync(0xffffffffu, depth_of(ti), 0);
+      const int ncols = __shfl_sync(0xffffffffu, ti.ncols, 0);
+      const int bc = kPair ? ncols >> 1 : ncols;  // columns this CTA loads
+      const int ch = __shfl_sync(0xffffffffu, ti.m0, 0) + rank * a.tile_m;
+      const int col = __shfl_sync(0xffffffffu, ti.c0, 0) + rank * bc;
+      const int row0 = __shfl_sync(0xffffffffu, ti.row0, 0);
+      const int phys = __shfl_sync(0xffffffffu, ti.phys, 0);
+      const int b_bytes = kBChanMajor ? ceil_div(bc, 64) * kSlabBytes : bc * kLine;
+      for (int d0 = 0; d0 < depth; d0 += step_depth) {
+        if (!mbar_wait(&empty[s], par)) {
           *s_abort = 1;
           break;
         }
-        uint8_t* stage = ring + (size_t)s * a.stage_bytes;
-        const int left = depth - ks * kDepthStage;
-        if (kKind == kGgGradW && left < kDepthStage && (left & 15)) clear_tail(stage, left, ti.ncols, lane);
-        tc::fence_after_sync();
-        if (lane == 0) {
-          const int kmax = min(kDepthStage / kDepthMma, ceil_div(left, kDepthMma));
-          const uint32_t sa = smem_u32(stage);
-          const uint32_t sb = sa + kABytes;
-          for (int kk = 0; kk < kmax; ++kk) {
-            const uint64_t da = kAChanMajor ? tc::mnmajor_sw128_desc(sa + kk * 2048, kSlabBytes)
-                                            : tc::kmajor_sw128_desc(sa + kk * 32);
-            const uint64_t db = kBChanMajor ? tc::mnmajor_sw128_desc(sb + kk * 2048, kSlabBytes)
-                                            : tc::kmajor_sw128_desc(sb + kk * 32);
-            if (kKind == kGgInt8)
-              tc::mma_i8(d_tmem, da, db, idesc, (ks | kk) != 0 ? 1u : 0u);
-            else
-              tc::mma_bf16(d_tmem, da, db, idesc, (ks | kk) != 0 ? 1u : 0u);
+        uint8_t* st = ring + s * (uint32_t)a.stage_bytes;
+        const int left = depth - d0;
+        const int nb = left >= step_depth ? a.blocks : ceil_div(left, kDepthBlock);
+        const bool rag = ragged(left);
+        if (rag) {
+          tails |= 1u << s;
+          tail_use ^= 1u << s;
+        } else {
+          tails &= ~(1u << s);
+        }
+        if (tc::elect_one()) {
+          const uint32_t bytes = nb * (a.a_block + b_bytes);
+          uint64_t* bar = rag ? &tail[s] : &full[s];
+          // the pair's copies are counted together on the even CTA's barrier (a ragged stage's on each CTA's own)
+          if (rag) {
+            mbar_arrive_expect_tx(bar, bytes);
+            if (rank == 0) mbar_arrive(&full[s]);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(bar, kPair ? 2 * bytes : bytes);
           }
-          tc::commit(&empty[s]);
+          const uint32_t bar_pair = kPair ? cluster_addr(bar, rag ? rank : 0) : 0;
+          auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
+            if constexpr (kPair) tma_load_2d_pair(dst, m, c0, c1, bar_pair, pol);
+            else tma_load_2d(dst, m, c0, c1, bar, pol);
+          };
+          auto load3 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1, int c2) {
+            if constexpr (kPair) tma_load_3d_pair(dst, m, c0, c1, c2, bar_pair, pol);
+            else tma_load_3d(dst, m, c0, c1, c2, bar, pol);
+          };
+          for (int b = 0; b < nb; ++b) {
+            uint8_t* sa = st + b * a.a_block;
+            uint8_t* sb = st + a.blocks * a.a_block + b * a.b_block;
+            const int d = d0 + b * kDepthBlock;
+            if constexpr (kKind == kGgGradW) {
+              for (int i = 0; i < 2; ++i) load2(sa + i * kSlabBytes, &a.tm_a, (ch + 64 * i) * 2, row0 + d);
+              for (int i = 0; i * 64 < bc; ++i) load2(sb + i * kSlabBytes, &a.tm_b, (col + 64 * i) * 2, row0 + d);
+            } else {
+              if constexpr (kKind == kGgGradX) {
+                for (int i = 0; i < 2; ++i) load3(sa + i * kSlabBytes, &a.tm_a, (ch + 64 * i) * 2, d, phys);
+              } else {
+                load3(sa, &a.tm_a, d * kElem, ch, phys);
+              }
+              int i = 0;
+              for (; i + kBoxBig <= bc; i += kBoxBig) load2(sb + i * kLine, &a.tm_b, d * kElem, row0 + col + i);
+              for (; i < bc; i += kBoxSmall) load2(sb + i * kLine, &a.tm_b16, d * kElem, row0 + col + i);
+            }
+          }
+        }
+        __syncwarp();
+        ++cnt;
+        if (++s == (uint32_t)a.stages) {
+          s = 0;
+          par ^= 1;
+        }
+      }
+    }
+    // Before the block may leave, every copy has landed and every arrival at
+    // this CTA's barriers has come: the last uses of the stages are free again.
+    bool fine = !*s_abort;
+    const uint32_t first = cnt > (uint32_t)a.stages ? cnt - a.stages : 0;
+    for (uint32_t c = first; fine && c < cnt; ++c) fine = mbar_wait(&empty[c % a.stages], (c / a.stages) & 1u);
+    if (!fine) {  // given up somewhere: the copies alone
+      for (uint32_t c = first; rank == 0 && c < cnt; ++c)
+        if (!mbar_wait(&full[c % a.stages], (c / a.stages) & 1u)) break;
+      for (int i = 0; i < a.stages; ++i)
+        if ((tails >> i & 1u) && !mbar_wait(&tail[i], (tail_use >> i & 1u) ^ 1u)) break;
+    }
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    // (The odd CTA of a pair only clears its half of the ragged stages.)
+    uint32_t s = 0, par = 0, tail_par = 0;
+    int i = 0;
+    const uint32_t sa0 = smem_u32(ring), sb0 = sa0 + a.blocks * a.a_block;
+    const uint64_t a_desc0 = kAChanMajor ? tc::mnmajor_sw128_desc(sa0, kSlabBytes) : tc::kmajor_sw128_desc(sa0);
+    const uint64_t b_desc0 = kBChanMajor ? tc::mnmajor_sw128_desc(sb0, kSlabBytes) : tc::kmajor_sw128_desc(sb0);
+    for (int t = unit; t < total_tiles; t += units, ++i) {
+      const Tile ti = decode(t);
+      const int depth = __shfl_sync(0xffffffffu, depth_of(ti), 0);
+      const int ncols = __shfl_sync(0xffffffffu, ti.ncols, 0);
+      const int bc = kPair ? ncols >> 1 : ncols;
+      const int buf = i & 1;
+      if (kKind != kGgGradW && rank != 0) break;
+      if (rank == 0) {
+        if (*s_abort || !mbar_wait<kPair>(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+          *s_abort = 1;
+          break;
+        }
+        tc::fence_after_sync();
+      }
+      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * a.col_cap);
+      const uint32_t idesc = a.idesc | ((uint32_t)(ncols >> 3) << 17);
+      for (int d0 = 0; d0 < depth; d0 += step_depth) {
+        uint8_t* st = ring + (size_t)s * a.stage_bytes;
+        const int left = depth - d0;
+        if (rank == 0 && !mbar_wait<kPair>(&full[s], par)) {
+          *s_abort = 1;
+          break;
+        }
+        if (ragged(left)) {
+          if (!mbar_wait(&tail[s], (tail_par >> s) & 1u)) {
+            *s_abort = 1;
+            break;
+          }
+          clear_tail(st, left, 2, lane);
+          clear_tail(st + a.a_block, left, ceil_div(bc, 64), lane);
+          if (kPair) {
+            if (rank != 0) {
+              if (lane == 0) mbar_arrive_cluster(cluster_addr(&peer[s], 0));
+            } else if (!mbar_wait<true>(&peer[s], (tail_par >> s) & 1u)) {
+              *s_abort = 1;
+              break;
+            }
+          }
+          tail_par ^= 1u << s;
+        }
+        if (rank == 0) {
+          tc::fence_after_sync();
+          // Descriptors count in 16 bytes: the next MMA's operands lie 32 bytes (K-major) or 16 lines
+          // (channel-major) on, the next block's a_block and b_block.  The whole warp runs this loop and
+          // one lane is elected at the instructions: with values the compiler knows to be the same in all
+          // lanes it keeps them in uniform registers, where the MMA wants them.
+          constexpr int kStepA = kAChanMajor ? 128 : 2, kStepB = kBChanMajor ? 128 : 2;
+          uint64_t da = a_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
+          uint64_t db = b_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
+          uint32_t more = d0 != 0;
+          for (int l = left; l > 0 && l > left - step_depth; l -= kDepthBlock) {
+            if (l >= kDepthBlock) {
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc::mma_g<kPair, kKind == kGgInt8>(d_tmem, da + kk * kStepA, db + kk * kStepB, idesc,
+                                                     kk == 0 ? more : 1u);
+              }
+            } else {
+              for (int kk = 0; kk * kDepthMma < l; ++kk)
+                if (tc::elect_one())
+                  tc::mma_g<kPair, kKind == kGgInt8>(d_tmem, da + kk * kStepA, db + kk * kStepB, idesc,
+                                                     kk == 0 ? more : 1u);
+            }
+            more = 1;
+            da += (uint32_t)a.a_block >> 4;
+            db += (uint32_t)a.b_block >> 4;
+          }
+          if (tc::elect_one()) tc::commit_g<kPair>(&empty[s]);  // frees the stage once these MMAs have read it
         }
         __syncwarp();
         if (++s == (uint32_t)a.stages) {
@@ -341,25 +461,22 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
         }
       }
       if (*s_abort) break;
-      if (lane == 0) {
-        if (steps > 0)
-          tc::commit(&acc_full[buf]);
-        else
-          mbar_arrive(&acc_full[buf]);  // an empty group: the epilogue writes zeros
-      }
+      if (rank == 0 && tc::elect_one()) tc::commit_g<kPair>(&acc_full[buf]);  // (an empty group: at once)
       __syncwarp();
     }
-    if (lane == 0) {  // every MMA of this CTA has completed before TMEM is freed
-      tc::commit(drain);
+    if (rank == 0) {  // every MMA has completed before TMEM is freed
+      if (tc::elect_one()) tc::commit_own<kPair>(drain);
       mbar_wait(drain, 0);
     }
     __syncwarp();
   } else {
     // ================================================================ epilogue
     const int q = warp & 3;  // TMEM lane quadrant of this warp
-    uint8_t* buf_t = epi + (warp - 2) * kEpiBytes;
+    uint8_t* stage_o = epi + (warp - 2) * kEpiBytes;
+    const int osz = a.out_dtype == MOE_T_FP32 ? 4 : 2;
     int i = 0;
-    for (int t = blockIdx.x; t < total_tiles; t += gridDim.x, ++i) {
+    uint32_t flip = 0;
+    for (int t = unit; t < total_tiles; t += units, ++i) {
       const Tile ti = decode(t);
       const int buf = i & 1;
       if (*s_abort || !mbar_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
@@ -368,124 +485,183 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
       }
       tc::fence_after_sync();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.col_cap);
-      const int ch0 = ti.m0 + q * 32;
-      if (kKind == kGgGradW) {
-        // one row n of dw per thread, 16 columns k at a time
-        const int n = ch0 + lane;
-        const bool zero = ti.n == 0;
-        for (int j0 = 0; j0 < ti.ncols; j0 += 16) {
-          uint32_t v[16];
-          tc::ld_32x32b_x16(taddr + j0, v);
-          tc::ld_wait();
-          if (zero) {
+      const int ch0 = ti.m0 + rank * a.tile_m + q * 32;
+      const bool mine = q * 32 < a.tile_m && ch0 < a.channels;
+      if (!mine) {
+      } else if constexpr (kKind == kGgGradW) {
+        // 32 rows n of dw, 128 bytes of k at a time: a thread packs its row's
+        // line into the swizzled block, one TMA store takes the block
+        const int per_line = 128 / osz;
+        for (int j0 = 0; j0 < ti.nc; j0 += per_line) {
+          uint32_t w[32];
+          if (ti.n == 0) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0u;
+            for (int j = 0; j < 32; ++j) w[j] = 0u;
+          } else if (osz == 4) {
+            tc::ld_cols32(taddr + j0, w);
+          } else {
+            uint32_t v[32];
+            tc::ld_cols32(taddr + j0, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = pack16(a.out_dtype, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            if (j0 + 32 < ti.nc) tc::ld_cols32(taddr + j0 + 32, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[16 + j] = pack16(a.out_dtype, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
           }
-          if (n < a.channels) {
-            const int64_t o = (int64_t)ti.expert * a.stride_o + (int64_t)n * a.ldo + ti.c0 + j0;
-            const bool whole = a.vec_ok && j0 + 16 <= ti.nc && !a.accumulate;
-            if (whole && a.out_dtype == MOE_T_FP32) {
-              uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(a.out) + o);
+          uint8_t* blk = stage_o + flip * 4096;
+          flip ^= 1;
+          if (a.tma_out) {  // the store before the last one has read this block
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+          }
+          uint4* line = reinterpret_cast<uint4*>(blk + lane * 128);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) d[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            } else if (whole) {
-              uint32_t p[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                p[j] = pack16(a.out_dtype, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-              uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o);
-              d[0] = make_uint4(p[0], p[1], p[2], p[3]);
-              d[1] = make_uint4(p[4], p[5], p[6], p[7]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (j0 + j >= ti.nc) break;
-                float f = __uint_as_float(v[j]);
-                if (a.accumulate) f += static_cast<float*>(a.out)[o + j];
-                store_one(a.out, a.out_dtype, o + j, f);
+          for (int c = 0; c < 8; ++c)
+            line[c ^ (lane & 7)] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          if (a.tma_out) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (a.accumulate)
+                tma_add_3d(&a.tm_o, blk, ti.c0 + j0, ch0, ti.expert);
+              else
+                tma_store_3d(&a.tm_o, blk, ti.c0 + j0, ch0, ti.expert);
+              bulk_commit();
+            }
+            __syncwarp();
+          } else {
+            // pitches that are not whole 16 bytes: plain stores, a row's values side by side
+            __syncwarp();
+            const int64_t o = (int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0 + j0;
+            const int n = min(32, a.channels - ch0), width = min(per_line, ti.nc - j0);
+            for (int r = 0; r < n; ++r) {
+              const uint32_t word =
+                  *reinterpret_cast<const uint32_t*>(blk + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+              if (osz == 4) {
+                float* d = static_cast<float*>(a.out) + o + r * a.ldo + lane;
+                if (lane < width) *d = a.accumulate ? *d + __uint_as_float(word) : __uint_as_float(word);
+              } else {
+                uint16_t* d = static_cast<uint16_t*>(a.out) + o + r * a.ldo + 2 * lane;
+                if (a.vec >= 4 && 2 * lane + 2 <= width) {
+                  *reinterpret_cast<uint32_t*>(d) = word;
+                } else {
+                  if (2 * lane < width) d[0] = (uint16_t)word;
+                  if (2 * lane + 1 < width) d[1] = (uint16_t)(word >> 16);
+                }
               }
             }
+            __syncwarp();
           }
         }
       } else {
-        // 16 rows x 32 channels at a time through shared memory, so that a
-        // row's 32 channels leave as 16-byte stores
+        // 32 rows x 32 channels at a time: a thread holds one channel of 32
+        // rows; through shared memory a row's channels leave side by side
         float sw = 0.f;
         if (kKind == kGgInt8 && ch0 + lane < a.channels)
           sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
         const int64_t row0 = (int64_t)ti.row0 + ti.c0;
-        const bool f32 = a.out_dtype == MOE_T_FP32;
-        for (int j0 = 0; j0 < ti.ncols; j0 += 16) {
-          uint32_t v[16];
-          tc::ld_32x32b_x16(taddr + j0, v);
-          tc::ld_wait();
-          if (kKind == kGgInt8) {
-            float sx = 0.f;
-            if (lane < 16 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              v[j] = __float_as_uint((float)(int)v[j] * (__shfl_sync(0xffffffffu, sx, j) * sw));
-          }
-          if (ch0 >= a.channels) continue;
+        const int pitch = osz == 4 ? kPitch32 : kPitch16;
+        const int width = min(32, a.channels - ch0) * osz;
+        for (int j0 = 0; j0 < ti.nc; j0 += 32) {
+          float sx = 0.f;
+          if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
           __syncwarp();
-          if (f32) {
-            float* b = reinterpret_cast<float*>(buf_t);
+          uint32_t v[32];
+          tc::ld_cols32(taddr + j0, v);
+          const int n = min(32, ti.nc - j0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) b[j * 36 + lane] = __uint_as_float(v[j]);
-          } else {
-            uint16_t* b = reinterpret_cast<uint16_t*>(buf_t);
+          for (int g = 0; g < 32; g += 8) {
+            if (g >= n) break;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              b[j * 40 + lane] = (uint16_t)pack16(a.out_dtype, __uint_as_float(v[j]), 0.f);
-          }
-          __syncwarp();
-          const int per = f32 ? 4 : 8;  // channels per 16-byte store
-          const int chunks = 32 / per;
-          for (int i2 = lane; i2 < 16 * chunks; i2 += 32) {
-            const int j = i2 / chunks, c = (i2 - j * chunks) * per;
-            if (j0 + j >= ti.nc || ch0 + c >= a.channels) continue;
-            const int64_t o = (row0 + j0 + j) * a.ldo + ch0 + c;
-            const uint8_t* src = buf_t + (f32 ? (j * 36 + c) * 4 : (j * 40 + c) * 2);
-            if (a.vec_ok && ch0 + c + per <= a.channels) {
-              const uint4 w = *reinterpret_cast<const uint4*>(src);
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + o * (f32 ? 4 : 2)) = w;
-            } else {
-              for (int z = 0; z < per && ch0 + c + z < a.channels; ++z) {
-                if (f32)
-                  static_cast<float*>(a.out)[o + z] = reinterpret_cast<const float*>(src)[z];
-                else
-                  static_cast<uint16_t*>(a.out)[o + z] = reinterpret_cast<const uint16_t*>(src)[z];
-              }
+            for (int j = g; j < g + 8; ++j) {
+              float f = __uint_as_float(v[j]);
+              if constexpr (kKind == kGgInt8) f = (float)(int)v[j] * (__shfl_sync(0xffffffffu, sx, j) * sw);
+              if (osz == 4)
+                *reinterpret_cast<float*>(stage_o + j * kPitch32 + lane * 4) = f;
+              else
+                *reinterpret_cast<uint16_t*>(stage_o + j * kPitch16 + lane * 2) = (uint16_t)pack16(a.out_dtype, f, 0.f);
             }
           }
+          __syncwarp();
+          uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
+          const int64_t op = a.ldo * osz;
+          if (a.vec == 16)
+            store_rows<16>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
+          else if (a.vec == 8)
+            store_rows<8>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
+          else if (a.vec == 4)
+            store_rows<4>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
+          else
+            store_rows<2>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
+          __syncwarp();
         }
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) {
+        if (kPair)
+          mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        else
+          mbar_arrive(&acc_empty[buf]);
+      }
+    }
+    if (kKind == kGgGradW && a.tma_out) {
+      if (lane == 0) bulk_wait_all();
+      __syncwarp();
     }
   }
+  __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (kPair) cluster_sync_all();  // the peer's arrivals and copies need this CTA's shared memory until here
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tmem_base, a.tmem_cols);
+  __syncwarp();
+  if (warp == 1) tc::tmem_dealloc_g<kPair>(tmem_base, a.tmem_cols);
 }
 
 // ------------------------------------------------------------------ host side
-template <int kKind>
-static cudaError_t launch_kind(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
-  cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind>>(smem);
+namespace {
+
+template <int kKind, bool kPair>
+cudaError_t launch_kind(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
+  cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind, kPair>>(smem);
   if (err != cudaSuccess) return err;
   static const char* const names[4] = {"grouped_gemm", "grouped_gemm_grad_x", "grouped_gemm_grad_w",
                                        "grouped_gemm_i8"};
   ProfScope prof(names[kKind], st);
-  return launch_pdl(grouped_gemm_kernel<kKind>, dim3(grid), dim3(kGgThreads), smem, st, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kGgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kKind, kPair>, a);
 }
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
 
 cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max, cudaStream_t st,
                                 int* unsupported) {
   *unsupported = 0;
   GgArgs a;
+  std::memset(&a, 0, sizeof(a));
   const int elem = p.kind == kGgInt8 ? 1 : 2;
   const bool gw = p.kind == kGgGradW, gx = p.kind == kGgGradX;
   a.offsets = p.offsets;
@@ -504,20 +680,40 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   a.out_dtype = p.out_dtype;
   a.accumulate = p.accumulate;
   const int osz = p.out_dtype == MOE_T_FP32 ? 4 : 2;
-  a.vec_ok = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && (p.ldo * osz) % 16 == 0 &&
-             (!gw || (p.stride_o * osz) % 16 == 0);
-  // Widest column tile: twice the rows an expert has on average, as tiles of
-  // 256 columns cost shared memory that small groups would rather have as
-  // more stages of weights in flight.
-  const int64_t groups = p.E < p.rows ? p.E : (p.rows > 0 ? p.rows : 1);
-  const int64_t avg2 = 2 * (((int64_t)p.rows + groups - 1) / groups);
-  const int64_t width = gw ? p.K : avg2;
-  a.col_cap = width <= 32 ? 32 : width <= 64 ? 64 : width <= 128 ? 128 : 256;
-  a.box_rows = 32;
-  a.stage_bytes = kABytes + a.col_cap * (gw && a.col_cap < 64 ? 256 : 128);
-  a.tmem_cols = 2 * a.col_cap;
+  const uint64_t place = reinterpret_cast<uint64_t>(p.out) | (uint64_t)p.ldo * osz | (gw ? (uint64_t)p.stride_o * osz : 0);
+  a.vec = place & 1 ? 1 : place & 2 ? 2 : place & 4 ? 4 : place & 8 ? 8 : 16;
+
+  // Tiles.  cap: the widest column tile, twice the rows an expert has on
+  // average, so that small groups leave the shared memory to stages of weights.
+  const int64_t groups = p.rows <= 0 ? 1 : p.E < p.rows ? p.E : p.rows;
+  const int64_t width = gw ? p.K : 2 * div_up(p.rows, groups);
+  int cap = width <= 16 ? 16 : width <= 32 ? 32 : width <= 64 ? 64 : width <= 128 ? 128 : 256;
+  const bool pair = gw || cap >= 128;
+  if (gw && cap < 128) cap = 128;
+  a.col_cap = cap;
+  a.col_step = gw ? 64 : pair ? 32 : 16;
+  const int64_t col_tiles = gw ? p.E * div_up(p.K, cap) : groups + p.rows / cap;
+  a.tile_m = 128;
+  a.blocks = pair ? 1 : 2;
+  if (!pair && !gx) {
+    // Few rows: the time is that of the weights, and of the SM with the most
+    // tiles.  Lower tiles even that out (16 KB of weights a stage all the same).
+    int64_t best = -1;
+    for (int m = 128; m >= 32; m >>= 1) {
+      const int64_t waves = div_up(groups * div_up(a.channels, m), n_sms) * m;
+      if (best < 0 || waves * 10 < best * 9) {
+        best = waves;
+        a.tile_m = m;
+      }
+    }
+    a.blocks = 256 / a.tile_m;
+  }
+  a.a_block = gx || gw ? 2 * kSlabBytes : a.tile_m * kLine;
+  a.b_block = (pair ? cap / 2 : cap) * kLine;
+  a.stage_bytes = a.blocks * (a.a_block + a.b_block);
+  a.tmem_cols = cap < 32 ? 64 : 2 * cap;  // (the epilogue reads 32 columns at a time)
   const size_t table = (size_t)(p.E + 1) * sizeof(Group);
-  const size_t fixed_bytes = 1024 + kEpiWarps * kEpiBytes + (2 * kMaxStages + 8) * 8 + 32 + table;
+  const size_t fixed_bytes = 1024 + kEpiWarps * epi_bytes(p.kind) + (4 * kMaxStages + 8) * 8 + 32 + table;
   int stages = (int)(((size_t)smem_max - fixed_bytes) / a.stage_bytes);
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) {
@@ -526,48 +722,55 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   }
   a.stages = stages;
   const size_t smem = fixed_bytes + (size_t)stages * a.stage_bytes;
-  if (p.kind == kGgInt8)
-    a.idesc = tc::idesc_i8_s32(kChan);
-  else
-    a.idesc = tc::idesc_16_f32(kChan, p.dtype == MOE_T_BF16, gx || gw, gw);
-  // tensor maps (dimensions in bytes along the rows)
-  if (gw && p.rows == 0) {  // nothing to load, every group is empty
-    std::memset(&a.tm_a, 0, sizeof(a.tm_a));
-    std::memset(&a.tm_b, 0, sizeof(a.tm_b));
-  } else if (gw) {
-    const uint64_t da[2] = {(uint64_t)p.N * 2, (uint64_t)p.rows}, sa[1] = {(uint64_t)p.lda_bytes};
-    const uint64_t db[2] = {(uint64_t)p.K * 2, (uint64_t)p.rows}, sb[1] = {(uint64_t)p.ldb_bytes};
-    const uint32_t box[2] = {128, 64};
-    if (!encode_tmap_u8(&a.tm_a, p.a, 2, da, sa, box, true) || !encode_tmap_u8(&a.tm_b, p.b, 2, db, sb, box, true)) {
-      *unsupported = 1;
-      return cudaSuccess;
+  const int m = pair ? 256 : 128;
+  a.idesc = p.kind == kGgInt8 ? tc::idesc_i8_s32(m) : tc::idesc_16_f32(m, p.dtype == MOE_T_BF16, gx || gw, gw);
+
+  // tensor maps (operands in bytes along the rows)
+  bool ok = true;
+  if (gw) {
+    if (p.rows > 0) {
+      const uint64_t da[2] = {(uint64_t)p.N * 2, (uint64_t)p.rows}, sa[1] = {(uint64_t)p.lda_bytes};
+      const uint64_t db[2] = {(uint64_t)p.K * 2, (uint64_t)p.rows}, sb[1] = {(uint64_t)p.ldb_bytes};
+      const uint32_t box[2] = {128, 64};
+      ok = encode_tmap_u8(&a.tm_a, p.a, 2, da, sa, box, true) && encode_tmap_u8(&a.tm_b, p.b, 2, db, sb, box, true);
+    }
+    if (ok && a.vec == 16) {
+      const CUtensorMapDataType t = p.out_dtype == MOE_T_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                    : p.out_dtype == MOE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      const uint64_t d[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.E};
+      const uint64_t s[2] = {(uint64_t)p.ldo * osz, (uint64_t)p.stride_o * osz};
+      const uint32_t box[3] = {(uint32_t)(128 / osz), 32, 1};
+      a.tma_out = encode_tmap_typed(&a.tm_o, t, p.out, 3, d, s, box) ? 1 : 0;
     }
   } else {
     const uint64_t da[3] = {(uint64_t)p.K * elem, (uint64_t)p.N, (uint64_t)p.n_phys};
     const uint64_t sa[2] = {(uint64_t)p.lda_bytes, (uint64_t)p.stride_w_bytes};
-    const uint32_t box_a[3] = {128, gx ? 64u : (uint32_t)kChan, 1};
+    const uint32_t box_a[3] = {128, gx ? 64u : (uint32_t)a.tile_m, 1};
     const uint64_t db[2] = {(uint64_t)(gx ? p.N : p.K) * elem, (uint64_t)p.rows}, sb[1] = {(uint64_t)p.ldb_bytes};
-    const uint32_t box_b[2] = {128, (uint32_t)a.box_rows};
-    if (!encode_tmap_u8(&a.tm_a, p.a, 3, da, sa, box_a, true) ||
-        !encode_tmap_u8(&a.tm_b, p.b, 2, db, sb, box_b, true)) {
-      *unsupported = 1;
-      return cudaSuccess;
-    }
+    const uint32_t box_b[2] = {128, kBoxBig}, box_b16[2] = {128, kBoxSmall};
+    ok = encode_tmap_u8(&a.tm_a, p.a, 3, da, sa, box_a, true) && encode_tmap_u8(&a.tm_b, p.b, 2, db, sb, box_b, true) &&
+         encode_tmap_u8(&a.tm_b16, p.b, 2, db, sb, box_b16, true);
   }
-  const int64_t m_tiles = (a.channels + kChan - 1) / kChan;
-  const int64_t col_tiles = gw ? (int64_t)p.E * ((p.K + a.col_cap - 1) / a.col_cap)
-                               : groups + p.rows / a.col_cap;
-  const int64_t max_tiles = m_tiles * col_tiles;
-  if (max_tiles > (int64_t)1 << 30) {
+  const int64_t max_tiles = div_up(a.channels, pair ? 2 * a.tile_m : a.tile_m) * col_tiles;
+  if (!ok || max_tiles > (int64_t)1 << 30) {
     *unsupported = 1;
     return cudaSuccess;
   }
+  if (pair) {
+    const int grid = 2 * (int)(max_tiles < n_sms / 2 ? max_tiles : n_sms / 2);
+    switch (p.kind) {
+      case kGgForward: return launch_kind<kGgForward, true>(a, grid, smem, st);
+      case kGgGradX: return launch_kind<kGgGradX, true>(a, grid, smem, st);
+      case kGgGradW: return launch_kind<kGgGradW, true>(a, grid, smem, st);
+      default: return launch_kind<kGgInt8, true>(a, grid, smem, st);
+    }
+  }
   const int grid = (int)(max_tiles < n_sms ? max_tiles : n_sms);
   switch (p.kind) {
-    case kGgForward: return launch_kind<kGgForward>(a, grid, smem, st);
-    case kGgGradX: return launch_kind<kGgGradX>(a, grid, smem, st);
-    case kGgGradW: return launch_kind<kGgGradW>(a, grid, smem, st);
-    default: return launch_kind<kGgInt8>(a, grid, smem, st);
+    case kGgForward: return launch_kind<kGgForward, false>(a, grid, smem, st);
+    case kGgGradX: return launch_kind<kGgGradX, false>(a, grid, smem, st);
+    default: return launch_kind<kGgInt8, false>(a, grid, smem, st);
   }
 }
 
