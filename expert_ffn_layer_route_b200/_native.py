@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional, Sequence
 
@@ -70,7 +71,7 @@ _LIB = None
 _P = ctypes.c_void_p
 _DP = ctypes.POINTER(LayerDesc)
 _WP = ctypes.POINTER(Weights)
-_GP = ctypes.POINTER(GemmDesc)
+_GP = _P  # a GemmDesc by its address
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
 
 _SIGS = {
@@ -235,44 +236,36 @@ def moe_layer_forward(desc, x, w_router, logit_bias, routed: Weights, shared: Op
 
 # ---------------------------------------------------------------------------
 # Expert operators.  These take whole tensors and read sizes, types and pitches
-# off them, so they also check them: the C entry points see only pointers.
+# off them, so they also check them: the C entry points see only pointers.  A
+# single-token call takes the GPU a few microseconds, so what depends on sizes,
+# pitches and types alone is checked once for each combination of them (the
+# cached functions below; a refusal raises and is not kept).
 
-_DTYPE = {}  # torch dtype -> moe_dtype, filled on first use (torch is imported late)
+_TYPE = {}  # torch dtype -> moe_dtype, filled on first use (torch is imported late)
+_torch = _raw_stream = _current = None
 
 
-def _dtypes():
-    if not _DTYPE:
-        import torch
+def _setup():
+    global _torch, _raw_stream, _current
+    import torch
 
-        _DTYPE.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3})
-    return _DTYPE
+    lib()
+    _TYPE.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3})
+    _raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
 
 
 def _refuse(where: str, why: str):
     raise MoeError(1, f"{where}: {why}")
 
 
-def _rows_of(t, rows, cols, where, name) -> int:
-    """Pitch of a [rows][cols] tensor whose rows are contiguous."""
-    if t.dim() != 2:
-        _refuse(where, f"{name} has {t.dim()} dimensions, 2 are wanted")
-    if tuple(t.shape) != (rows, cols):
-        _refuse(where, f"{name} has shape {tuple(t.shape)}, ({rows}, {cols}) is wanted")
-    s = t.stride()
-    if s[1] != 1 and cols > 1:
+def _pitch(shape, stride, rows, cols, where, name) -> int:
+    """Row pitch of what has to be a [rows][cols] matrix of contiguous rows."""
+    if shape != (rows, cols):
+        _refuse(where, f"{name} has shape {tuple(shape)}, ({rows}, {cols}) is wanted")
+    if stride[1] != 1 and cols > 1:
         _refuse(where, f"{name}'s rows are not contiguous")
-    return s[0] if rows > 1 else (cols + 15) // 16 * 16
-
-
-def _matrices_of(t, E, N, K, where, name):
-    """(row pitch, distance of the matrices) of an [E][N][K] tensor."""
-    if t.dim() != 3 or t.shape[1] != N or t.shape[2] != K or (E is not None and t.shape[0] != E):
-        _refuse(where, f"{name} has shape {tuple(t.shape)}, ({'E' if E is None else E}, {N}, {K}) is wanted")
-    s = t.stride()
-    if s[2] != 1 and K > 1:
-        _refuse(where, f"{name}'s rows are not contiguous")
-    ld = s[1] if N > 1 else (K + 15) // 16 * 16
-    return ld, (s[0] if t.shape[0] > 1 else N * ld)
+    return stride[0] if rows > 1 else (cols + 15) & -16
 
 
 def _vector(t, n, dtype, where, name):
@@ -280,200 +273,195 @@ def _vector(t, n, dtype, where, name):
         _refuse(where, f"{name} has to be a contiguous {dtype} vector of at least {n} values")
 
 
-def _place(where, stream, *tensors):
-    """(device index, raw stream) of a call on these tensors, which have to lie on one GPU."""
-    import torch
+@functools.lru_cache(maxsize=1024)
+def _gemm_desc(where, w_name, w, w_stride, w_type, x_name, x, x_stride, x_type, y_name, y, y_stride, y_type, off,
+               off_stride, off_type, by_slots, a_type, b_type, out_type):
+    """(description, its address, rows, experts, matrices, N) of a grouped product: w [M][N][K], x [R][K],
+    y [R][N] and offsets [E + 1], by their shapes, strides and types; a_type, b_type, out_type: the types of the
+    two operands and of the result."""
+    if len(w) != 3:
+        _refuse(where, f"{w_name} has {len(w)} dimensions, 3 are wanted")
+    M, N, K = w
+    if len(off) != 1 or off[0] < 2 or off_type != _torch.int32 or off_stride[0] != 1:
+        _refuse(where, "offsets has to be a contiguous int32 vector of E + 1 values")
+    E = off[0] - 1
+    if not by_slots and M != E:
+        _refuse(where, f"{M} matrices for {E} experts (a slot_map would say which is whose)")
+    R = x[0] if len(x) else -1
+    int8 = where == "moe_grouped_gemm_i8"
+    t, to = _TYPE.get(a_type, 9), _TYPE.get(out_type, 9)
+    if a_type != b_type or to > 2 or (t != 3 if int8 else t > 1):
+        _refuse(where, f"types {a_type}, {b_type} -> {out_type}")
+    ld_x = _pitch(x, x_stride, R, K, where, x_name)
+    ld_y = _pitch(y, y_stride, R, N, where, y_name)
+    if w_stride[2] != 1 and K > 1:
+        _refuse(where, f"{w_name}'s rows are not contiguous")
+    ld_w = w_stride[1] if N > 1 else (K + 15) & -16
+    d = GemmDesc(R, E, N, K, t, to, M, ld_x, ld_y, ld_w, w_stride[0] if M > 1 else N * ld_w)
+    return d, ctypes.addressof(d), R, E, M, N
 
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device != dev):
-            _refuse(where, "the tensors have to be on one CUDA device")
+
+def _call(where, index, f, stream, *args):
+    """f(*args, stream) on GPU `index`; stream None: the current one there."""
     if stream is None:
-        return dev.index, torch._C._cuda_getCurrentRawStream(dev.index)
-    return dev.index, stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _launch(where, index, call, *args):
-    """call(*args) with device `index` current."""
-    import torch
-
-    if torch._C._cuda_getDevice() == index:
-        status = call(*args)
+        stream = _raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if _current() == index:
+        status = f(*args, stream)
     else:
-        with torch.cuda.device(index):
-            status = call(*args)
+        with _torch.cuda.device(index):
+            status = f(*args, stream)
     if status != MOE_OK:
         raise MoeError(status, where)
 
 
-def _groups(offsets, slot_map, E_w, where):
-    """Number of experts of a grouped product (E from offsets, checked against the matrices)."""
-    import torch
-
-    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != torch.int32 or offsets.stride(0) != 1:
-        _refuse(where, "offsets has to be a contiguous int32 vector of E + 1 values")
-    E = offsets.shape[0] - 1
-    if slot_map is not None:
-        _vector(slot_map, E, torch.int32, where, "slot_map")
-    elif E_w != E:
-        _refuse(where, f"{E_w} matrices for {E} experts (a slot_map would say which is whose)")
-    return E
+def _one_gpu(where, *tensors) -> int:
+    """Index of the GPU that all of the tensors lie on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            index = -1
+    if index < 0:
+        _refuse(where, "the tensors have to be on one CUDA device")
+    return index
 
 
 def moe_grouped_gemm(x, w, offsets, out, slot_map=None, stream=None):
     """out[r] = x[r] w[e]^T for the rows r of each expert e (x [R][K], w [E][N][K], out [R][N])."""
     where = "moe_grouped_gemm"
-    types = _dtypes()
-    if w.dim() != 3:
-        _refuse(where, "w has to be [E][N][K]")
-    Ew, N, K = w.shape
-    E = _groups(offsets, slot_map, Ew, where)
-    R = x.shape[0]
-    if x.dtype != w.dtype or types.get(x.dtype, 9) > 1 or types.get(out.dtype, 9) > 2:
-        _refuse(where, f"types {x.dtype}, {w.dtype} -> {out.dtype}")
-    ldx = _rows_of(x, R, K, where, "x")
-    ldy = _rows_of(out, R, N, where, "out")
-    ldw, sw = _matrices_of(w, None, N, K, where, "w")
-    d = GemmDesc(R, E, N, K, types[x.dtype], types[out.dtype], Ew, ldx, ldy, ldw, sw)
-    dev, st = _place(where, stream, x, w, offsets, out, slot_map)
-    _launch(where, dev, lib().moe_grouped_gemm, d, x.data_ptr(), w.data_ptr(), _ptr(slot_map), offsets.data_ptr(),
-            out.data_ptr(), st)
+    if _torch is None:
+        _setup()
+    _, d, _, E, _, _ = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "x", x.shape, x.stride(), x.dtype, "out",
+                                  out.shape, out.stride(), out.dtype, offsets.shape, offsets.stride(), offsets.dtype,
+                                  slot_map is not None, x.dtype, w.dtype, out.dtype)
+    if slot_map is not None:
+        _vector(slot_map, E, _torch.int32, where, "slot_map")
+    _call(where, _one_gpu(where, x, w, offsets, out, slot_map), _LIB.moe_grouped_gemm, stream, d, x.data_ptr(),
+          w.data_ptr(), _ptr(slot_map), offsets.data_ptr(), out.data_ptr())
 
 
 def moe_grouped_gemm_grad_x(dy, w, offsets, dx, slot_map=None, stream=None):
     """dx[r] = dy[r] w[e] for the rows r of each expert e (dy [R][N], w [E][N][K], dx [R][K])."""
     where = "moe_grouped_gemm_grad_x"
-    types = _dtypes()
-    if w.dim() != 3:
-        _refuse(where, "w has to be [E][N][K]")
-    Ew, N, K = w.shape
-    E = _groups(offsets, slot_map, Ew, where)
-    R = dy.shape[0]
-    if dy.dtype != w.dtype or types.get(dy.dtype, 9) > 1 or types.get(dx.dtype, 9) > 2:
-        _refuse(where, f"types {dy.dtype}, {w.dtype} -> {dx.dtype}")
-    ldy = _rows_of(dy, R, N, where, "dy")
-    ldx = _rows_of(dx, R, K, where, "dx")
-    ldw, sw = _matrices_of(w, None, N, K, where, "w")
-    d = GemmDesc(R, E, N, K, types[dy.dtype], types[dx.dtype], Ew, ldx, ldy, ldw, sw)
-    dev, st = _place(where, stream, dy, w, offsets, dx, slot_map)
-    _launch(where, dev, lib().moe_grouped_gemm_grad_x, d, dy.data_ptr(), w.data_ptr(), _ptr(slot_map),
-            offsets.data_ptr(), dx.data_ptr(), st)
+    if _torch is None:
+        _setup()
+    _, d, _, E, _, _ = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "dx", dx.shape, dx.stride(), dx.dtype,
+                                  "dy", dy.shape, dy.stride(), dy.dtype, offsets.shape, offsets.stride(),
+                                  offsets.dtype, slot_map is not None, dy.dtype, w.dtype, dx.dtype)
+    if slot_map is not None:
+        _vector(slot_map, E, _torch.int32, where, "slot_map")
+    _call(where, _one_gpu(where, dy, w, offsets, dx, slot_map), _LIB.moe_grouped_gemm_grad_x, stream, d,
+          dy.data_ptr(), w.data_ptr(), _ptr(slot_map), offsets.data_ptr(), dx.data_ptr())
 
 
 def moe_grouped_gemm_grad_w(dy, x, offsets, dw, accumulate=False, stream=None):
     """dw[e] (+)= dy[rows of e]^T x[rows of e] (dy [R][N], x [R][K], dw [E][N][K])."""
     where = "moe_grouped_gemm_grad_w"
-    types = _dtypes()
-    if dw.dim() != 3:
-        _refuse(where, "dw has to be [E][N][K]")
-    E, N, K = dw.shape
-    _groups(offsets, None, E, where)
-    R = x.shape[0]
-    if x.dtype != dy.dtype or types.get(x.dtype, 9) > 1 or types.get(dw.dtype, 9) > 2:
-        _refuse(where, f"types {dy.dtype}, {x.dtype} -> {dw.dtype}")
-    ldx = _rows_of(x, R, K, where, "x")
-    ldy = _rows_of(dy, R, N, where, "dy")
-    ldw, sw = _matrices_of(dw, E, N, K, where, "dw")
-    d = GemmDesc(R, E, N, K, types[x.dtype], types[dw.dtype], 0, ldx, ldy, ldw, sw)
-    dev, st = _place(where, stream, dw, x, dy, offsets)
-    _launch(where, dev, lib().moe_grouped_gemm_grad_w, d, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(),
-            dw.data_ptr(), 1 if accumulate else 0, st)
+    if _torch is None:
+        _setup()
+    _, d, _, _, _, _ = _gemm_desc(where, "dw", dw.shape, dw.stride(), dw.dtype, "x", x.shape, x.stride(), x.dtype,
+                                  "dy", dy.shape, dy.stride(), dy.dtype, offsets.shape, offsets.stride(),
+                                  offsets.dtype, False, dy.dtype, x.dtype, dw.dtype)
+    _call(where, _one_gpu(where, dy, x, offsets, dw), _LIB.moe_grouped_gemm_grad_w, stream, d, dy.data_ptr(),
+          x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), 1 if accumulate else 0)
 
 
 def moe_grouped_gemm_i8(x, x_scale, w, w_scale, offsets, out, slot_map=None, stream=None):
     """out[r][n] = x_scale[r] w_scale[e][n] sum_k x[r][k] w[e][n][k] over int8 codes x [R][K], w [E][N][K]."""
-    import torch
-
     where = "moe_grouped_gemm_i8"
-    types = _dtypes()
-    if w.dim() != 3:
-        _refuse(where, "w has to be [E][N][K]")
-    Ew, N, K = w.shape
-    E = _groups(offsets, slot_map, Ew, where)
-    R = x.shape[0]
-    if x.dtype != torch.int8 or w.dtype != torch.int8 or types.get(out.dtype, 9) > 2:
-        _refuse(where, f"types {x.dtype}, {w.dtype} -> {out.dtype}")
-    ldx = _rows_of(x, R, K, where, "x")
-    ldy = _rows_of(out, R, N, where, "out")
-    ldw, sw = _matrices_of(w, None, N, K, where, "w")
-    _vector(x_scale, R, torch.float32, where, "x_scale")
-    if tuple(w_scale.shape) != (Ew, N) or w_scale.dtype != torch.float32 or not w_scale.is_contiguous():
-        _refuse(where, f"w_scale has to be a contiguous float32 tensor of shape ({Ew}, {N})")
-    d = GemmDesc(R, E, N, K, 3, types[out.dtype], Ew, ldx, ldy, ldw, sw)
-    dev, st = _place(where, stream, x, x_scale, w, w_scale, offsets, out, slot_map)
-    _launch(where, dev, lib().moe_grouped_gemm_i8, d, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
-            w_scale.data_ptr(), _ptr(slot_map), offsets.data_ptr(), out.data_ptr(), st)
+    if _torch is None:
+        _setup()
+    _, d, R, E, M, N = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "x", x.shape, x.stride(), x.dtype, "out",
+                                  out.shape, out.stride(), out.dtype, offsets.shape, offsets.stride(), offsets.dtype,
+                                  slot_map is not None, x.dtype, w.dtype, out.dtype)
+    _vector(x_scale, R, _torch.float32, where, "x_scale")
+    if w_scale.shape != (M, N) or w_scale.dtype != _torch.float32 or not w_scale.is_contiguous():
+        _refuse(where, f"w_scale has to be a contiguous float32 tensor of shape ({M}, {N})")
+    if slot_map is not None:
+        _vector(slot_map, E, _torch.int32, where, "slot_map")
+    _call(where, _one_gpu(where, x, x_scale, w, w_scale, offsets, out, slot_map), _LIB.moe_grouped_gemm_i8, stream, d,
+          x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _ptr(slot_map), offsets.data_ptr(),
+          out.data_ptr())
+
+
+@functools.lru_cache(maxsize=1024)
+def _quant_sizes(where, x, x_stride, x_type, q, q_stride, q_type, gather):
+    """(rows, K, type, pitch of x, rows of x, pitch of q)"""
+    if len(x) != 2 or len(q) != 2:
+        _refuse(where, "x and q have to be matrices")
+    t = _TYPE.get(x_type, 9)
+    if t > 1 or q_type != _torch.int8:
+        _refuse(where, f"types {x_type} -> {q_type}")
+    if not gather and x[0] != q[0]:
+        _refuse(where, f"{x[0]} rows of x, {q[0]} of q")
+    K = x[1]
+    return q[0], K, t, _pitch(x, x_stride, x[0], K, where, "x"), x[0], _pitch(q, q_stride, q[0], K, where, "q")
 
 
 def moe_quant_rows_i8(x, q, scale, row_token=None, stream=None):
     """int8 codes q [R][K] and scale [R] of the rows of x, or of x[row_token[r]] (a dropped row: zeros)."""
-    import torch
-
     where = "moe_quant_rows_i8"
-    types = _dtypes()
-    if x.dim() != 2 or q.dim() != 2:
-        _refuse(where, "x and q have to be matrices")
-    T, K = x.shape
-    R = q.shape[0]
-    if types.get(x.dtype, 9) > 1 or q.dtype != torch.int8:
-        _refuse(where, f"types {x.dtype} -> {q.dtype}")
-    if row_token is None:
-        if T != R:
-            _refuse(where, f"{T} rows of x, {R} of q")
-    else:
-        _vector(row_token, R, torch.int32, where, "row_token")
-    ldx = _rows_of(x, T, K, where, "x")
-    ldq = _rows_of(q, R, K, where, "q")
-    _vector(scale, R, torch.float32, where, "scale")
-    dev, st = _place(where, stream, x, q, scale, row_token)
-    _launch(where, dev, lib().moe_quant_rows_i8, R, K, types[x.dtype], x.data_ptr(), ldx, _ptr(row_token), T,
-            q.data_ptr(), ldq, scale.data_ptr(), st)
+    if _torch is None:
+        _setup()
+    R, K, t, ld_x, T, ld_q = _quant_sizes(where, x.shape, x.stride(), x.dtype, q.shape, q.stride(), q.dtype,
+                                          row_token is not None)
+    if row_token is not None:
+        _vector(row_token, R, _torch.int32, where, "row_token")
+    _vector(scale, R, _torch.float32, where, "scale")
+    _call(where, _one_gpu(where, x, q, scale, row_token), _LIB.moe_quant_rows_i8, stream, R, K, t, x.data_ptr(), ld_x,
+          _ptr(row_token), T, q.data_ptr(), ld_q, scale.data_ptr())
 
 
-def _gate_up(gate_up, where):
-    if gate_up.dim() != 2 or gate_up.shape[1] % 2 or _dtypes().get(gate_up.dtype, 9) > 1:
+@functools.lru_cache(maxsize=1024)
+def _swiglu_sizes(where, gu, gu_stride, gu_type, *others):
+    """(rows, F, type, pitch of gate_up, pitches of the others); others: name, factor of F, shape, stride, type."""
+    t = _TYPE.get(gu_type, 9)
+    if len(gu) != 2 or gu[1] & 1 or t > 1:
         _refuse(where, "gate_up has to be a bf16 or fp16 matrix [R][2F]")
-    R, F2 = gate_up.shape
-    return R, F2 // 2, _rows_of(gate_up, R, F2, where, "gate_up")
+    R, F = gu[0], gu[1] >> 1
+    out = [R, F, t, _pitch(gu, gu_stride, R, 2 * F, where, "gate_up")]
+    for i in range(0, len(others), 5):
+        name, factor, shape, stride, dtype = others[i: i + 5]
+        if dtype != (_torch.int8 if name == "q" else gu_type):
+            _refuse(where, f"types {gu_type} -> {dtype}")
+        out.append(_pitch(shape, stride, R, factor * F, where, name))
+    return out
 
 
 def moe_swiglu(gate_up, h, stream=None):
     """h = silu(gate_up[:, :F]) * gate_up[:, F:] (h [R][F])."""
     where = "moe_swiglu"
-    R, F, ldg = _gate_up(gate_up, where)
-    if h.dtype != gate_up.dtype:
-        _refuse(where, f"types {gate_up.dtype} -> {h.dtype}")
-    ldh = _rows_of(h, R, F, where, "h")
-    dev, st = _place(where, stream, gate_up, h)
-    _launch(where, dev, lib().moe_swiglu, R, F, _DTYPE[h.dtype], gate_up.data_ptr(), ldg, h.data_ptr(), ldh, st)
+    if _torch is None:
+        _setup()
+    R, F, t, ld, ld_h = _swiglu_sizes(where, gate_up.shape, gate_up.stride(), gate_up.dtype, "h", 1, h.shape,
+                                      h.stride(), h.dtype)
+    _call(where, _one_gpu(where, gate_up, h), _LIB.moe_swiglu, stream, R, F, t, gate_up.data_ptr(), ld, h.data_ptr(),
+          ld_h)
 
 
 def moe_swiglu_quant_i8(gate_up, q, scale, stream=None):
     """int8 codes q [R][F] and scale [R] of silu(gate_up[:, :F]) * gate_up[:, F:]."""
-    import torch
-
     where = "moe_swiglu_quant_i8"
-    R, F, ldg = _gate_up(gate_up, where)
-    if q.dtype != torch.int8:
-        _refuse(where, f"types {gate_up.dtype} -> {q.dtype}")
-    ldq = _rows_of(q, R, F, where, "q")
-    _vector(scale, R, torch.float32, where, "scale")
-    dev, st = _place(where, stream, gate_up, q, scale)
-    _launch(where, dev, lib().moe_swiglu_quant_i8, R, F, _DTYPE[gate_up.dtype], gate_up.data_ptr(), ldg,
-            q.data_ptr(), ldq, scale.data_ptr(), st)
+    if _torch is None:
+        _setup()
+    R, F, t, ld, ld_q = _swiglu_sizes(where, gate_up.shape, gate_up.stride(), gate_up.dtype, "q", 1, q.shape,
+                                      q.stride(), q.dtype)
+    _vector(scale, R, _torch.float32, where, "scale")
+    _call(where, _one_gpu(where, gate_up, q, scale), _LIB.moe_swiglu_quant_i8, stream, R, F, t, gate_up.data_ptr(),
+          ld, q.data_ptr(), ld_q, scale.data_ptr())
 
 
 def moe_swiglu_grad(gate_up, dh, dgate_up, stream=None):
     """dgate_up [R][2F], the gradient of moe_swiglu at gate_up for a given dh [R][F]; it may be gate_up itself."""
     where = "moe_swiglu_grad"
-    R, F, ldg = _gate_up(gate_up, where)
-    if dh.dtype != gate_up.dtype or dgate_up.dtype != gate_up.dtype:
-        _refuse(where, f"types {gate_up.dtype}, {dh.dtype} -> {dgate_up.dtype}")
-    ldh = _rows_of(dh, R, F, where, "dh")
-    ldd = _rows_of(dgate_up, R, 2 * F, where, "dgate_up")
-    dev, st = _place(where, stream, gate_up, dh, dgate_up)
-    _launch(where, dev, lib().moe_swiglu_grad, R, F, _DTYPE[dh.dtype], gate_up.data_ptr(), ldg, dh.data_ptr(), ldh,
-            dgate_up.data_ptr(), ldd, st)
+    if _torch is None:
+        _setup()
+    R, F, t, ld, ld_h, ld_d = _swiglu_sizes(where, gate_up.shape, gate_up.stride(), gate_up.dtype, "dh", 1, dh.shape,
+                                            dh.stride(), dh.dtype, "dgate_up", 2, dgate_up.shape, dgate_up.stride(),
+                                            dgate_up.dtype)
+    _call(where, _one_gpu(where, gate_up, dh, dgate_up), _LIB.moe_swiglu_grad, stream, R, F, t, gate_up.data_ptr(), ld,
+          dh.data_ptr(), ld_h, dgate_up.data_ptr(), ld_d)
 
 
 def moe_get_last_error() -> int:

@@ -41,4 +41,7 @@ struct GroupedProblem {
 cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max, cudaStream_t st,
                                 int* unsupported);
 
+// The same products (forward, int8) for few rows: csrc/grouped_gemv.cu.
+cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,264 @@
+// The grouped products for a handful of rows (single-token decode), forward
+// and int8: see grouped_gemm.cu for the mathematics.
+//
+// With so few rows the time is that of the weights' bytes and of getting
+// started; 128-channel tensor-core tiles are too coarse to spread one token's
+// experts evenly over 148 SMs.  Here a warp takes 4 channels of one expert and
+// all of the expert's rows: each lane streams 16-byte pieces of the 4 weight
+// rows past the activations (L1 keeps those), in fp32 (int8: exact int32 by
+// 4-way dot products), and a butterfly adds the lanes.  Nothing is staged and
+// nothing waits, so the loads in flight are only bounded by the resident
+// warps: 8 x 16 bytes per lane.
+#include "grouped_gemm.cuh"
+
+#include "common.cuh"
+#include "launch.cuh"
+#include "profile.cuh"
+
+namespace moe {
+
+namespace {
+
+#ifndef MINB
+#define MINB 3
+#endif
+constexpr int kGvThreads = 256;
+constexpr int kGvMinBlocks = MINB;
+constexpr int kGvChan = 4;                             // channels per warp
+constexpr int kGvBlockChan = kGvThreads / 32 * kGvChan;  // per block
+
+struct GemvArgs {
+  const uint8_t* w;
+  const uint8_t* x;
+  const int32_t* offsets;
+  const int32_t* slot_map;
+  const float* x_scale;
+  const float* w_scale;
+  void* out;
+  int64_t lda, ldb, stride_w;  // bytes
+  int64_t ldo;                 // elements
+  int E, rows, n_phys, channels, depth_bytes;
+  int out_dtype;
+};
+
+enum { kBf16 = MOE_T_BF16, kFp16 = MOE_T_FP16, kI8 = MOE_T_INT8 };
+
+// Weights pass once: they need no place in L1.
+__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// The first n bytes of a 16-byte piece, zeros behind them (what lies behind a
+// row's end may be anything, a NaN too).
+__device__ __forceinline__ uint4 keep(uint4 v, int n) {
+  uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = n - 4 * i;
+    e[i] = b >= 4 ? e[i] : b <= 0 ? 0u : e[i] & (0xffffffffu >> (32 - 8 * b));
+  }
+  return v;
+}
+
+template <int kType>
+struct Sum {
+  using T = float;
+};
+template <>
+struct Sum<kI8> {
+  using T = int;
+};
+
+template <int kType>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+  const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kType == kBf16) {
+      f[2 * i] = __uint_as_float(e[i] << 16);
+      f[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u);
+    } else {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&e[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
+}
+
+// acc[c][r] += the dot product of 16 bytes of channel c's and row r's values.
+template <int kType, int R>
+__device__ __forceinline__ void dot(const uint4 (&w)[kGvChan], const uint4 (&x)[R],
+                                    typename Sum<kType>::T (&acc)[kGvChan][R]) {
+  if constexpr (kType == kI8) {
+#pragma unroll
+    for (int c = 0; c < kGvChan; ++c)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        acc[c][r] = __dp4a((int)w[c].x, (int)x[r].x, acc[c][r]);
+        acc[c][r] = __dp4a((int)w[c].y, (int)x[r].y, acc[c][r]);
+        acc[c][r] = __dp4a((int)w[c].z, (int)x[r].z, acc[c][r]);
+        acc[c][r] = __dp4a((int)w[c].w, (int)x[r].w, acc[c][r]);
+      }
+  } else {
+    float xf[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) unpack<kType>(x[r], xf[r]);
+#pragma unroll
+    for (int c = 0; c < kGvChan; ++c) {
+      float wf[8];
+      unpack<kType>(w[c], wf);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[c][r] = fmaf(wf[i], xf[r][i], acc[c][r]);
+    }
+  }
+}
+
+// R rows from `row` on, the warp's channels from ch0 on.
+template <int kType, int R>
+__device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0, int phys, int lane) {
+  using S = typename Sum<kType>::T;
+  const uint8_t* w[kGvChan];
+  const uint8_t* x[R];
+#pragma unroll
+  for (int c = 0; c < kGvChan; ++c)  // (past the last channel: the last again, not stored)
+    w[c] = a.w + phys * a.stride_w + min(ch0 + c, a.channels - 1) * a.lda;
+#pragma unroll
+  for (int r = 0; r < R; ++r) x[r] = a.x + (row + r) * a.ldb;
+  S acc[kGvChan][R];
+#pragma unroll
+  for (int c = 0; c < kGvChan; ++c)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[c][r] = 0;
+  const int whole = a.depth_bytes & ~15;
+  int b = lane * 16;
+  for (; b + 512 < whole; b += 1024) {
+    uint4 w0[kGvChan], w1[kGvChan], x0[R], x1[R];
+#pragma unroll
+    for (int c = 0; c < kGvChan; ++c) w0[c] = load_stream(w[c] + b);
+#pragma unroll
+    for (int c = 0; c < kGvChan; ++c) w1[c] = load_stream(w[c] + b + 512);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x0[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b));
+      x1[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b + 512));
+    }
+    dot<kType, R>(w0, x0, acc);
+    dot<kType, R>(w1, x1, acc);
+  }
+  for (; b < a.depth_bytes; b += 512) {
+    const int n = a.depth_bytes - b;
+    uint4 w0[kGvChan], x0[R];
+#pragma unroll
+    for (int c = 0; c < kGvChan; ++c) w0[c] = load_stream(w[c] + b);
+#pragma unroll
+    for (int r = 0; r < R; ++r) x0[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b));
+    if (n < 16) {
+#pragma unroll
+      for (int c = 0; c < kGvChan; ++c) w0[c] = keep(w0[c], n);
+#pragma unroll
+      for (int r = 0; r < R; ++r) x0[r] = keep(x0[r], n);
+    }
+    dot<kType, R>(w0, x0, acc);
+  }
+#pragma unroll
+  for (int c = 0; c < kGvChan; ++c)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[c][r] += __shfl_xor_sync(0xffffffffu, acc[c][r], o);
+  if (lane < kGvChan * R) {
+    const int lr = lane / kGvChan, ch = ch0 + lane % kGvChan;
+    S s = 0;
+#pragma unroll
+    for (int c = 0; c < kGvChan; ++c)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r * kGvChan + c == lane) s = acc[c][r];
+    if (ch < a.channels) {
+      float f = (float)s;
+      if constexpr (kType == kI8)
+        f *= __ldg(a.x_scale + row + lr) * __ldg(a.w_scale + (int64_t)phys * a.channels + ch);
+      const int64_t o = (row + lr) * a.ldo + ch;
+      if (a.out_dtype == MOE_T_FP32)
+        static_cast<float*>(a.out)[o] = f;
+      else if (a.out_dtype == MOE_T_BF16)
+        static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(f);
+      else
+        static_cast<__half*>(a.out)[o] = __float2half_rn(f);
+    }
+  }
+}
+
+}  // namespace
+
+// Grid: (channel blocks, rows); the blocks of a group's first row serve the
+// whole group, those of its other rows end at once, so that a group's weights
+// are read once whatever the routing.
+template <int kType>
+__global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(const GemvArgs a) {
+  __shared__ int s_n, s_phys;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int row = blockIdx.y;
+  if (tid == 0) s_n = 0;
+  pdl_wait_and_trigger();
+  __syncthreads();
+  for (int e = tid; e < a.E; e += kGvThreads) {
+    const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+    if (lo < 0 || hi < lo || hi > a.rows) {
+      set_status(MOE_ERR_DEVICE_INDEX);
+    } else if (lo == row && hi > lo) {
+      int p = e, n = hi - lo;
+      if (a.slot_map) {
+        p = __ldg(a.slot_map + e);
+        if (p < 0 || p >= a.n_phys) {
+          if (p != -1) set_status(MOE_ERR_DEVICE_INDEX);
+          n = 0;  // not resident: its rows are left as they are
+        }
+      }
+      s_phys = p;
+      s_n = n;
+    }
+  }
+  __syncthreads();
+  const int n = s_n, phys = s_phys;
+  const int ch0 = blockIdx.x * kGvBlockChan + (tid >> 5) * kGvChan;
+  if (n == 0 || ch0 >= a.channels) return;
+  int r = 0;
+  for (; r + 2 <= n; r += 2) rows_of<kType, 2>(a, row + r, ch0, phys, lane);
+  if (r < n) rows_of<kType, 1>(a, row + r, ch0, phys, lane);
+}
+
+cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st) {
+  GemvArgs a;
+  a.w = static_cast<const uint8_t*>(p.a);
+  a.x = static_cast<const uint8_t*>(p.b);
+  a.offsets = p.offsets;
+  a.slot_map = p.slot_map;
+  a.x_scale = p.x_scale;
+  a.w_scale = p.w_scale;
+  a.out = p.out;
+  a.lda = p.lda_bytes;
+  a.ldb = p.ldb_bytes;
+  a.stride_w = p.stride_w_bytes;
+  a.ldo = p.ldo;
+  a.E = p.E;
+  a.rows = p.rows;
+  a.n_phys = p.n_phys;
+  a.channels = p.N;
+  a.depth_bytes = p.K * (p.kind == kGgInt8 ? 1 : 2);
+  a.out_dtype = p.out_dtype;
+  ProfScope prof(p.kind == kGgInt8 ? "grouped_gemm_i8" : "grouped_gemm", st);
+  const dim3 grid((p.N + kGvBlockChan - 1) / kGvBlockChan, p.rows);
+  auto k = p.kind == kGgInt8           ? grouped_gemv_kernel<kI8>
+           : p.dtype == MOE_T_BF16 ? grouped_gemv_kernel<kBf16>
+                                       : grouped_gemv_kernel<kFp16>;
+  return launch_pdl(k, grid, dim3(kGvThreads), 0, st, a);
+}
+
+}  // namespace moe
