@@ -1,6 +1,4 @@
 // C entry points of the expert operators: argument checks, then one launch each.
-#include <cstdlib>
-
 #include "devinfo.cuh"
 #include "expert_rows.cuh"
 #include "grouped_gemm.cuh"
@@ -43,13 +41,10 @@ moe_status check_gemm(const moe_gemm_desc* d, bool int8, Pitch* t) {
   return MOE_OK;
 }
 
-// (for measuring) rows up to which the few-row kernel runs
-const int kFewRows = getenv("MOE_FEW") ? atoi(getenv("MOE_FEW")) : 16;
-
 moe_status run(const GroupedProblem& p, void* stream) {
   const DevInfo di = dev_info();
   int unsupported = 0;
-  if ((p.kind == kGgForward || p.kind == kGgInt8) && p.rows <= kFewRows) {
+  if (grouped_gemv_pays(p)) {
     const cudaError_t err = launch_grouped_gemv(p, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }

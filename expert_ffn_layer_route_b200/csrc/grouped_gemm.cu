@@ -27,24 +27,25 @@ namespace moe {
 
 namespace {
 
+constexpr int kChan = 128;             // channels per CTA and tile: the TMEM lanes
 constexpr int kLine = 128;             // bytes of the contraction per K-major block (one swizzle line)
 constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction rows x 64 channels of 16 bits
+constexpr int kABlock = kChan * kLine;  // the channels' operand of a block, either way
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 4;
 constexpr int kGgThreads = 32 * (2 + kEpiWarps);
 constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of the ragged operand
 
 // Staging buffer of one epilogue warp: 32 rows x 32 channels (forward, grad_x,
-// int8; rows padded against bank conflicts), or two 32-row blocks of 128-byte
-// swizzled lines that TMA stores read (grad_w).
+// int8; rows padded against bank conflicts), or 32 lines of 128 bytes, their
+// 16-byte pieces swizzled (grad_w).
 constexpr int kPitch16 = 80, kPitch32 = 144;
-constexpr int epi_bytes(int kind) { return kind == kGgGradW ? 2 * 32 * 128 : 5 * 1024; }
+constexpr int epi_bytes(int kind) { return kind == kGgGradW ? 32 * 128 : 5 * 1024; }
 
 struct alignas(64) GgArgs {
   CUtensorMap tm_a;
   CUtensorMap tm_b;    // 64-row boxes
   CUtensorMap tm_b16;  // 16-row boxes
-  CUtensorMap tm_o;    // grad_w's result
   const int32_t* offsets;
   const int32_t* slot_map;
   const float* x_scale;
@@ -55,21 +56,22 @@ struct alignas(64) GgArgs {
   int channels;  // M extent: N (forward, grad_w, int8) or K (grad_x)
   int depth;     // contraction extent in elements (grad_w: the group's rows)
   int cols;      // grad_w: K
-  int tile_m;    // channels per CTA and tile (TMEM lanes in use)
   int col_cap;   // widest column tile
   int col_step;  // column tiles start on multiples of this
   int blocks;    // 128-byte contraction blocks per stage
-  int stages, a_block, b_block, stage_bytes, tmem_cols;
+  int stages, b_block, stage_bytes, tmem_cols;
   uint32_t idesc;  // instruction descriptor without N
   int out_dtype;
   int vec;        // widest store the result's address and pitches allow (bytes)
-  int tma_out;    // grad_w: tm_o is in use
   int accumulate;
 };
 
-// One group's entry in the shared-memory table.
-struct Group {
+// One group's entry in the shared-memory table.  The divisions that a tile's
+// place needs are made once, when the table is built.
+struct alignas(16) Group {
   int tile0;  // first tile
+  int ct, w;  // column tiles, and their width
+  float per_ct;  // 1 / ct
   int row0, n;
   int expert, phys;
 };
@@ -77,10 +79,50 @@ struct Group {
 struct Tile {
   int m0;            // first channel (of the pair)
   int c0, nc;        // first column (row inside the group; grad_w: k) and columns that exist
-  int ncols;         // MMA N: nc rounded up
   int row0, n;       // the group's rows
   int expert, phys;
 };
+
+// A role's walk through the tiles t, t + units, ...: the group is looked for
+// from the last one on.
+struct Walk {
+  int g = 0;
+  __device__ __forceinline__ Tile at(int t, const Group* grp, int ngroups, int width_all, int tile_chan) {
+    if (g + 1 < ngroups && grp[g + 1].tile0 <= t) {
+      int lo = g + 1, hi = ngroups - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (grp[mid].tile0 <= t) lo = mid; else hi = mid - 1;
+      }
+      g = lo;
+    }
+    const int4 p = *reinterpret_cast<const int4*>(&grp[g]);
+    const int4 r = *(reinterpret_cast<const int4*>(&grp[g]) + 1);
+    const int local = t - p.x, ct = p.y;
+    // column tiles of one channel tile run side by side: local = mi * ct + ci
+    int mi = __float2int_rd((float)local * __int_as_float(p.w)), ci = local - mi * ct;
+    if (ci < 0) {
+      --mi;
+      ci += ct;
+    } else if (ci >= ct) {
+      ++mi;
+      ci -= ct;
+    }
+    Tile ti;
+    ti.m0 = mi * tile_chan;
+    ti.c0 = ci * p.z;
+    ti.nc = min(p.z, (width_all ? width_all : r.y) - ti.c0);
+    ti.row0 = r.x;
+    ti.n = r.y;
+    ti.expert = r.z;
+    ti.phys = r.w;
+    return ti;
+  }
+};
+
+// A value that is the same in all lanes, in a register the compiler knows to
+// be: what TMA and MMA instructions take their operands from.
+__device__ __forceinline__ int uni(int v) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)v); }
 
 __device__ __forceinline__ uint32_t pack16(int dtype, float lo, float hi) {
   if (dtype == MOE_T_BF16) {
@@ -104,6 +146,28 @@ __device__ __forceinline__ void clear_tail(uint8_t* block, int left, int slabs, 
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+__device__ __forceinline__ void st_global16(uint8_t* p, const uint4& v) {
+  asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Staged lines to global memory, every lane 16 bytes of a row at a time, all
+// loads before the first store: kPieces 16-byte pieces a row, rows [0, n) of
+// 32, all of a row's pieces wanted.  at(row, piece): the staged address.
+template <int kPieces, typename At>
+__device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, int n, int lane, At at) {
+  constexpr int kRows = 32 / kPieces;  // rows a warp stores at once
+  const int piece = lane % kPieces, r0 = lane / kPieces;
+  uint4 t[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) t[i] = lds128(at(r0 + i * kRows, piece));
+  uint8_t* d = out + r0 * pitch + piece * 16;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if (r0 + i * kRows < n) st_global16(d, t[i]);
+    d += kRows * pitch;
+  }
 }
 
 // One row's staged bytes to global memory in pieces of `vec` bytes, the pieces
@@ -147,14 +211,15 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   constexpr int kDepthMma = 32 / kElem;
   constexpr int kColRound = kPair ? 32 : 16;
   constexpr int kEpiBytes = epi_bytes(kKind);
+  constexpr int kTileChan = kPair ? 2 * kChan : kChan;
 
   const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, for the compiler too
+  const int warp = uni(tid >> 5);
   const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
   const int unit = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int units = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset: the compiler goes on knowing the space)
   uint8_t* ring = smem;
   uint8_t* epi = ring + (size_t)a.stages * a.stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(epi + kEpiWarps * kEpiBytes);
@@ -167,7 +232,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_ngroups = reinterpret_cast<int*>(s_tmem + 2);
-  Group* grp = reinterpret_cast<Group*>(s_tmem + 4);  // [E + 1], the groups that have tiles
+  Group* grp = reinterpret_cast<Group*>(s_tmem + 6);  // [E + 1], the groups that have tiles
 
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -208,19 +273,18 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   }
   __syncthreads();
   if (warp == 0) {
-    const int m_tiles = ceil_div(a.channels, kPair ? 2 * a.tile_m : a.tile_m);
+    const int m_tiles = ceil_div(a.channels, kTileChan);
     int ng = 0, tiles = 0;
     for (int base = 0; base < a.E; base += 32) {
       const int e = base + lane;
-      int row0 = 0, n = 0, p = 0, t = 0;
+      int row0 = 0, n = 0, p = 0, t = 0, ct = 0;
       if (e < a.E) {
         row0 = grp[e].row0;
         n = grp[e].n;
         p = grp[e].phys;
-        if (kKind == kGgGradW)  // a group without rows has zeros to write, unless they would be added
-          t = n == 0 && a.accumulate ? 0 : m_tiles * ceil_div(a.cols, a.col_cap);
-        else
-          t = m_tiles * ceil_div(n, a.col_cap);
+        // (grad_w: a group without rows has zeros to write, unless they would be added)
+        ct = kKind != kGgGradW ? ceil_div(n, a.col_cap) : n == 0 && a.accumulate ? 0 : ceil_div(a.cols, a.col_cap);
+        t = m_tiles * ct;
       }
       const uint32_t on = __ballot_sync(0xffffffffu, t > 0);
       int incl = t;
@@ -232,6 +296,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
       if (t > 0) {  // slots at or before this expert's own: already read above
         Group g;
         g.tile0 = tiles + incl - t;
+        g.ct = ct;
+        g.w = ceil_div(ceil_div(kKind == kGgGradW ? a.cols : n, ct), a.col_step) * a.col_step;  // as even as the step allows
+        g.per_ct = 1.f / (float)ct;
         g.row0 = row0;
         g.n = n;
         g.expert = e;
@@ -251,33 +318,13 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   __syncthreads();
   if constexpr (kPair) cluster_sync_all();  // the peer's barriers are initialised
   tc::fence_after_sync();
-  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *s_tmem, 0);
-  const int ngroups = __shfl_sync(0xffffffffu, *s_ngroups, 0);
-  const int total_tiles = __shfl_sync(0xffffffffu, grp[ngroups].tile0, 0);
+  const uint32_t tmem_base = uni(*s_tmem);
+  const int ngroups = uni(*s_ngroups);
+  const int total_tiles = uni(grp[ngroups].tile0);
 
-  auto decode = [&](int t) {
-    int lo = 0, hi = ngroups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (grp[mid].tile0 <= t) lo = mid; else hi = mid - 1;
-    }
-    const Group g = grp[lo];
-    Tile ti;
-    ti.row0 = g.row0;
-    ti.n = g.n;
-    ti.expert = g.expert;
-    ti.phys = g.phys;
-    const int local = t - g.tile0;
-    const int width = kKind == kGgGradW ? a.cols : g.n;
-    const int ct = ceil_div(width, a.col_cap);  // column tiles, as even as their step allows
-    const int w = ceil_div(ceil_div(width, ct), a.col_step) * a.col_step;
-    const int mi = local / ct;                  // column tiles of one channel tile run side by side
-    ti.m0 = mi * (kPair ? 2 * a.tile_m : a.tile_m);
-    ti.c0 = (local - mi * ct) * w;
-    ti.nc = min(w, width - ti.c0);
-    ti.ncols = (ti.nc + kColRound - 1) & ~(kColRound - 1);
-    return ti;
-  };
+  Walk walk;
+  auto tile_at = [&](int t) { return walk.at(t, grp, ngroups, kKind == kGgGradW ? a.cols : 0, kTileChan); };
+  auto mma_cols = [](const Tile& ti) { return (ti.nc + kColRound - 1) & ~(kColRound - 1); };
   const int step_depth = kDepthBlock * a.blocks;
   auto depth_of = [&](const Tile& ti) { return kKind == kGgGradW ? ti.n : a.depth; };
   // grad_w: whether a step ends inside a group of 16 contraction rows
@@ -295,14 +342,14 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     uint32_t s = 0, par = 1, cnt = 0, tails = 0, tail_use = 0;
     for (int t = unit; t < total_tiles; t += units) {
       if (*s_abort) break;
-      const Tile ti = decode(t);
-      const int depth = __shfl_sync(0xffffffffu, depth_of(ti), 0);
-      const int ncols = __shfl_sync(0xffffffffu, ti.ncols, 0);
+      const Tile ti = tile_at(t);
+      const int depth = uni(depth_of(ti));
+      const int ncols = uni(mma_cols(ti));
       const int bc = kPair ? ncols >> 1 : ncols;  // columns this CTA loads
-      const int ch = __shfl_sync(0xffffffffu, ti.m0, 0) + rank * a.tile_m;
-      const int col = __shfl_sync(0xffffffffu, ti.c0, 0) + rank * bc;
-      const int row0 = __shfl_sync(0xffffffffu, ti.row0, 0);
-      const int phys = __shfl_sync(0xffffffffu, ti.phys, 0);
+      const int ch = uni(ti.m0) + rank * kChan;
+      const int col = uni(ti.c0) + rank * bc;
+      const int row0 = uni(ti.row0);
+      const int phys = uni(ti.phys);
       const int b_bytes = kBChanMajor ? ceil_div(bc, 64) * kSlabBytes : bc * kLine;
       for (int d0 = 0; d0 < depth; d0 += step_depth) {
         if (!mbar_wait(&empty[s], par)) {
@@ -320,7 +367,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
           tails &= ~(1u << s);
         }
         if (tc::elect_one()) {
-          const uint32_t bytes = nb * (a.a_block + b_bytes);
+          const uint32_t bytes = nb * (kABlock + b_bytes);
           uint64_t* bar = rag ? &tail[s] : &full[s];
           // the pair's copies are counted together on the even CTA's barrier (a ragged stage's on each CTA's own)
           if (rag) {
@@ -339,8 +386,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
             else tma_load_3d(dst, m, c0, c1, c2, bar, pol);
           };
           for (int b = 0; b < nb; ++b) {
-            uint8_t* sa = st + b * a.a_block;
-            uint8_t* sb = st + a.blocks * a.a_block + b * a.b_block;
+            uint8_t* sa = st + b * kABlock;
+            uint8_t* sb = st + a.blocks * kABlock + b * a.b_block;
             const int d = d0 + b * kDepthBlock;
             if constexpr (kKind == kGgGradW) {
               for (int i = 0; i < 2; ++i) load2(sa + i * kSlabBytes, &a.tm_a, (ch + 64 * i) * 2, row0 + d);
@@ -381,13 +428,13 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     // (The odd CTA of a pair only clears its half of the ragged stages.)
     uint32_t s = 0, par = 0, tail_par = 0;
     int i = 0;
-    const uint32_t sa0 = smem_u32(ring), sb0 = sa0 + a.blocks * a.a_block;
+    const uint32_t sa0 = smem_u32(ring), sb0 = sa0 + a.blocks * kABlock;
     const uint64_t a_desc0 = kAChanMajor ? tc::mnmajor_sw128_desc(sa0, kSlabBytes) : tc::kmajor_sw128_desc(sa0);
     const uint64_t b_desc0 = kBChanMajor ? tc::mnmajor_sw128_desc(sb0, kSlabBytes) : tc::kmajor_sw128_desc(sb0);
     for (int t = unit; t < total_tiles; t += units, ++i) {
-      const Tile ti = decode(t);
-      const int depth = __shfl_sync(0xffffffffu, depth_of(ti), 0);
-      const int ncols = __shfl_sync(0xffffffffu, ti.ncols, 0);
+      const Tile ti = tile_at(t);
+      const int depth = uni(depth_of(ti));
+      const int ncols = uni(mma_cols(ti));
       const int bc = kPair ? ncols >> 1 : ncols;
       const int buf = i & 1;
       if (kKind != kGgGradW && rank != 0) break;
@@ -413,7 +460,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
             break;
           }
           clear_tail(st, left, 2, lane);
-          clear_tail(st + a.a_block, left, ceil_div(bc, 64), lane);
+          clear_tail(st + kABlock, left, ceil_div(bc, 64), lane);
           if (kPair) {
             if (rank != 0) {
               if (lane == 0) mbar_arrive_cluster(cluster_addr(&peer[s], 0));
@@ -449,7 +496,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
                                                      kk == 0 ? more : 1u);
             }
             more = 1;
-            da += (uint32_t)a.a_block >> 4;
+            da += kABlock >> 4;
             db += (uint32_t)a.b_block >> 4;
           }
           if (tc::elect_one()) tc::commit_g<kPair>(&empty[s]);  // frees the stage once these MMAs have read it
@@ -475,9 +522,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     uint8_t* stage_o = epi + (warp - 2) * kEpiBytes;
     const int osz = a.out_dtype == MOE_T_FP32 ? 4 : 2;
     int i = 0;
-    uint32_t flip = 0;
     for (int t = unit; t < total_tiles; t += units, ++i) {
-      const Tile ti = decode(t);
+      const Tile ti = tile_at(t);
       const int buf = i & 1;
       if (*s_abort || !mbar_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
         *s_abort = 1;
@@ -485,75 +531,109 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
       }
       tc::fence_after_sync();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.col_cap);
-      const int ch0 = ti.m0 + rank * a.tile_m + q * 32;
-      const bool mine = q * 32 < a.tile_m && ch0 < a.channels;
+      const int ch0 = ti.m0 + rank * kChan + q * 32;
+      const bool mine = ch0 < a.channels;
       if (!mine) {
       } else if constexpr (kKind == kGgGradW) {
-        // 32 rows n of dw, 128 bytes of k at a time: a thread packs its row's
-        // line into the swizzled block, one TMA store takes the block
+        // 32 rows n of dw, 128 bytes of k at a time: a thread holds one row's
+        // line; through shared memory the lines leave 8 lanes to a line
         const int per_line = 128 / osz;
+        uint8_t* const o = static_cast<uint8_t*>(a.out) +
+                           ((int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0) * osz;
+        const int64_t op = a.ldo * osz;
+        const int n = min(32, a.channels - ch0);
+        uint32_t v[32], v2[32];
+        tc::ld_issue32(taddr, v);
+        if (osz == 2) tc::ld_issue32(taddr + 32, v2);
         for (int j0 = 0; j0 < ti.nc; j0 += per_line) {
-          uint32_t w[32];
+          tc::ld_wait32(v);
+          uint4* line = reinterpret_cast<uint4*>(stage_o + lane * 128);
           if (ti.n == 0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = 0u;
+            for (int c = 0; c < 8; ++c) line[c ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
           } else if (osz == 4) {
-            tc::ld_cols32(taddr + j0, w);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              line[c ^ (lane & 7)] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
           } else {
-            uint32_t v[32];
-            tc::ld_cols32(taddr + j0, v);
+            tc::ld_wait32(v2);
+            auto two = [&](const uint32_t(&u)[32], int j) {
+              return pack16(a.out_dtype, __uint_as_float(u[j]), __uint_as_float(u[j + 1]));
+            };
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = pack16(a.out_dtype, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            if (j0 + 32 < ti.nc) tc::ld_cols32(taddr + j0 + 32, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[16 + j] = pack16(a.out_dtype, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-          }
-          uint8_t* blk = stage_o + flip * 4096;
-          flip ^= 1;
-          if (a.tma_out) {  // the store before the last one has read this block
-            if (lane == 0) bulk_wait_read<1>();
-            __syncwarp();
-          }
-          uint4* line = reinterpret_cast<uint4*>(blk + lane * 128);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            line[c ^ (lane & 7)] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-          if (a.tma_out) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (a.accumulate)
-                tma_add_3d(&a.tm_o, blk, ti.c0 + j0, ch0, ti.expert);
-              else
-                tma_store_3d(&a.tm_o, blk, ti.c0 + j0, ch0, ti.expert);
-              bulk_commit();
+            for (int c = 0; c < 4; ++c) {
+              line[c ^ (lane & 7)] = make_uint4(two(v, 8 * c), two(v, 8 * c + 2), two(v, 8 * c + 4), two(v, 8 * c + 6));
+              line[(c + 4) ^ (lane & 7)] =
+                  make_uint4(two(v2, 8 * c), two(v2, 8 * c + 2), two(v2, 8 * c + 4), two(v2, 8 * c + 6));
             }
-            __syncwarp();
-          } else {
-            // pitches that are not whole 16 bytes: plain stores, a row's values side by side
-            __syncwarp();
-            const int64_t o = (int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0 + j0;
-            const int n = min(32, a.channels - ch0), width = min(per_line, ti.nc - j0);
-            for (int r = 0; r < n; ++r) {
-              const uint32_t word =
-                  *reinterpret_cast<const uint32_t*>(blk + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
-              if (osz == 4) {
-                float* d = static_cast<float*>(a.out) + o + r * a.ldo + lane;
-                if (lane < width) *d = a.accumulate ? *d + __uint_as_float(word) : __uint_as_float(word);
-              } else {
-                uint16_t* d = static_cast<uint16_t*>(a.out) + o + r * a.ldo + 2 * lane;
-                if (a.vec >= 4 && 2 * lane + 2 <= width) {
-                  *reinterpret_cast<uint32_t*>(d) = word;
-                } else {
-                  if (2 * lane < width) d[0] = (uint16_t)word;
-                  if (2 * lane + 1 < width) d[1] = (uint16_t)(word >> 16);
+          }
+          __syncwarp();
+          if (j0 + per_line < ti.nc) {  // the next line's values come while this one's leave
+            tc::ld_issue32(taddr + j0 + per_line, v);
+            if (osz == 2) tc::ld_issue32(taddr + j0 + per_line + 32, v2);
+          }
+          const int width = min(128, (ti.nc - j0) * osz);
+          if (a.vec == 16 && width == 128 && !a.accumulate) {
+            const uint32_t base = smem_u32(stage_o);
+            store_lines<8>(o + j0 * osz, op, n, lane,
+                           [&](int r, int p) { return base + r * 128 + ((p ^ (r & 7)) << 4); });
+          } else if (a.vec == 16) {
+            const int piece = lane & 7, r0 = lane >> 3;
+            uint8_t* d = o + j0 * osz + r0 * op + piece * 16;
+            const bool whole = piece * 16 + 16 <= width;
+            if (a.accumulate) {
+#pragma unroll
+              for (int r = 0; r < 32; r += 4) {
+                float4 f = *reinterpret_cast<const float4*>(stage_o + (r0 + r) * 128 + ((piece ^ ((r0 + r) & 7)) << 4));
+                float* g = reinterpret_cast<float*>(d + r * op);
+                if (r0 + r < n) {
+                  if (whole) {
+                    const float4 h = *reinterpret_cast<const float4*>(g);
+                    *reinterpret_cast<float4*>(g) = make_float4(h.x + f.x, h.y + f.y, h.z + f.z, h.w + f.w);
+                  } else {
+                    const float e[4] = {f.x, f.y, f.z, f.w};
+                    for (int z = 0; z < 4; ++z)
+                      if (piece * 16 + z * 4 < width) g[z] += e[z];
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int r = 0; r < 32; r += 4) {
+                const uint8_t* sp = stage_o + (r0 + r) * 128 + ((piece ^ ((r0 + r) & 7)) << 4);
+                if (r0 + r < n) {
+                  if (whole)
+                    *reinterpret_cast<uint4*>(d + r * op) = *reinterpret_cast<const uint4*>(sp);
+                  else
+                    for (int z = 0; piece * 16 + z < width; z += osz) {
+                      if (osz == 4)
+                        *reinterpret_cast<uint32_t*>(d + r * op + z) = *reinterpret_cast<const uint32_t*>(sp + z);
+                      else
+                        *reinterpret_cast<uint16_t*>(d + r * op + z) = *reinterpret_cast<const uint16_t*>(sp + z);
+                    }
                 }
               }
             }
-            __syncwarp();
+          } else {
+            // rows that do not start on 16 bytes: a line at a time, 4 bytes a lane
+            uint8_t* d = o + j0 * osz + lane * 4;
+#pragma unroll 4
+            for (int r = 0; r < n; ++r, d += op) {
+              const uint32_t word = *reinterpret_cast<const uint32_t*>(
+                  stage_o + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+              if (osz == 4) {
+                float* g = reinterpret_cast<float*>(d);
+                if (lane * 4 < width) *g = a.accumulate ? *g + __uint_as_float(word) : __uint_as_float(word);
+              } else if (a.vec >= 4 && lane * 4 + 4 <= width) {
+                *reinterpret_cast<uint32_t*>(d) = word;
+              } else {
+                uint16_t* g = reinterpret_cast<uint16_t*>(d);
+                if (lane * 4 < width) g[0] = (uint16_t)word;
+                if (lane * 4 + 2 < width) g[1] = (uint16_t)(word >> 16);
+              }
+            }
           }
+          __syncwarp();
         }
       } else {
         // 32 rows x 32 channels at a time: a thread holds one channel of 32
@@ -564,12 +644,12 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
         const int64_t row0 = (int64_t)ti.row0 + ti.c0;
         const int pitch = osz == 4 ? kPitch32 : kPitch16;
         const int width = min(32, a.channels - ch0) * osz;
+        uint32_t v[32];
+        tc::ld_issue32(taddr, v);
         for (int j0 = 0; j0 < ti.nc; j0 += 32) {
           float sx = 0.f;
           if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
-          __syncwarp();
-          uint32_t v[32];
-          tc::ld_cols32(taddr + j0, v);
+          tc::ld_wait32(v);
           const int n = min(32, ti.nc - j0);
 #pragma unroll
           for (int g = 0; g < 32; g += 8) {
@@ -585,9 +665,15 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
             }
           }
           __syncwarp();
+          if (j0 + 32 < ti.nc) tc::ld_issue32(taddr + j0 + 32, v);  // comes while these rows leave
           uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
           const int64_t op = a.ldo * osz;
-          if (a.vec == 16)
+          const uint32_t base = smem_u32(stage_o);
+          if (a.vec == 16 && width == 128)
+            store_lines<8>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch32 + p * 16; });
+          else if (a.vec == 16 && osz == 2 && width == 64)
+            store_lines<4>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch16 + p * 16; });
+          else if (a.vec == 16)
             store_rows<16>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
           else if (a.vec == 8)
             store_rows<8>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
@@ -602,14 +688,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
       __syncwarp();
       if (lane == 0) {
         if (kPair)
-          mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+          mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
         else
           mbar_arrive(&acc_empty[buf]);
       }
-    }
-    if (kKind == kGgGradW && a.tma_out) {
-      if (lane == 0) bulk_wait_all();
-      __syncwarp();
     }
   }
   __syncwarp();
@@ -693,24 +775,9 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   a.col_cap = cap;
   a.col_step = gw ? 64 : pair ? 32 : 16;
   const int64_t col_tiles = gw ? p.E * div_up(p.K, cap) : groups + p.rows / cap;
-  a.tile_m = 128;
   a.blocks = pair ? 1 : 2;
-  if (!pair && !gx) {
-    // Few rows: the time is that of the weights, and of the SM with the most
-    // tiles.  Lower tiles even that out (16 KB of weights a stage all the same).
-    int64_t best = -1;
-    for (int m = 128; m >= 32; m >>= 1) {
-      const int64_t waves = div_up(groups * div_up(a.channels, m), n_sms) * m;
-      if (best < 0 || waves * 10 < best * 9) {
-        best = waves;
-        a.tile_m = m;
-      }
-    }
-    a.blocks = 256 / a.tile_m;
-  }
-  a.a_block = gx || gw ? 2 * kSlabBytes : a.tile_m * kLine;
-  a.b_block = (pair ? cap / 2 : cap) * kLine;
-  a.stage_bytes = a.blocks * (a.a_block + a.b_block);
+    a.b_block = (pair ? cap / 2 : cap) * kLine;
+  a.stage_bytes = a.blocks * (kABlock + a.b_block);
   a.tmem_cols = cap < 32 ? 64 : 2 * cap;  // (the epilogue reads 32 columns at a time)
   const size_t table = (size_t)(p.E + 1) * sizeof(Group);
   const size_t fixed_bytes = 1024 + kEpiWarps * epi_bytes(p.kind) + (4 * kMaxStages + 8) * 8 + 32 + table;
@@ -734,25 +801,16 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
       const uint32_t box[2] = {128, 64};
       ok = encode_tmap_u8(&a.tm_a, p.a, 2, da, sa, box, true) && encode_tmap_u8(&a.tm_b, p.b, 2, db, sb, box, true);
     }
-    if (ok && a.vec == 16) {
-      const CUtensorMapDataType t = p.out_dtype == MOE_T_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                    : p.out_dtype == MOE_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-      const uint64_t d[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.E};
-      const uint64_t s[2] = {(uint64_t)p.ldo * osz, (uint64_t)p.stride_o * osz};
-      const uint32_t box[3] = {(uint32_t)(128 / osz), 32, 1};
-      a.tma_out = encode_tmap_typed(&a.tm_o, t, p.out, 3, d, s, box) ? 1 : 0;
-    }
   } else {
     const uint64_t da[3] = {(uint64_t)p.K * elem, (uint64_t)p.N, (uint64_t)p.n_phys};
     const uint64_t sa[2] = {(uint64_t)p.lda_bytes, (uint64_t)p.stride_w_bytes};
-    const uint32_t box_a[3] = {128, gx ? 64u : (uint32_t)a.tile_m, 1};
+    const uint32_t box_a[3] = {128, gx ? 64u : (uint32_t)kChan, 1};
     const uint64_t db[2] = {(uint64_t)(gx ? p.N : p.K) * elem, (uint64_t)p.rows}, sb[1] = {(uint64_t)p.ldb_bytes};
     const uint32_t box_b[2] = {128, kBoxBig}, box_b16[2] = {128, kBoxSmall};
     ok = encode_tmap_u8(&a.tm_a, p.a, 3, da, sa, box_a, true) && encode_tmap_u8(&a.tm_b, p.b, 2, db, sb, box_b, true) &&
          encode_tmap_u8(&a.tm_b16, p.b, 2, db, sb, box_b16, true);
   }
-  const int64_t max_tiles = div_up(a.channels, pair ? 2 * a.tile_m : a.tile_m) * col_tiles;
+  const int64_t max_tiles = div_up(a.channels, pair ? 2 * kChan : kChan) * col_tiles;
   if (!ok || max_tiles > (int64_t)1 << 30) {
     *unsupported = 1;
     return cudaSuccess;

@@ -41,7 +41,9 @@ struct GroupedProblem {
 cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max, cudaStream_t st,
                                 int* unsupported);
 
-// The same products (forward, int8) for few rows: csrc/grouped_gemv.cu.
+// The same products (forward, int8) for few rows: csrc/grouped_gemv.cu, and
+// whether that kernel is the faster one.
+bool grouped_gemv_pays(const GroupedProblem& p);
 cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st);
 
 }  // namespace moe

@@ -19,11 +19,9 @@ namespace moe {
 
 namespace {
 
-#ifndef MINB
-#define MINB 3
-#endif
 constexpr int kGvThreads = 256;
-constexpr int kGvMinBlocks = MINB;
+constexpr int kGvMinBlocks = 3;  // 24 warps and 85 registers a thread: 2 / 4 / 5 blocks were 28.7 / 29.6 / 25.6 us
+                                 // for one token (3: 25.8), 26.4 / 25.5 / 26.1 us in int8 (25.6)
 constexpr int kGvChan = 4;                             // channels per warp
 constexpr int kGvBlockChan = kGvThreads / 32 * kGvChan;  // per block
 
@@ -232,6 +230,18 @@ __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(
   int r = 0;
   for (; r + 2 <= n; r += 2) rows_of<kType, 2>(a, row + r, ch0, phys, lane);
   if (r < n) rows_of<kType, 1>(a, row + r, ch0, phys, lane);
+}
+
+// Up to 12 rows (int8: 16) and about two per expert in use; measured against the
+// tensor-core kernel (us, this kernel first): gpt-oss-shaped bf16 gate/up, 128
+// experts, 4 / 8 / 12 / 16 rows 24.6 / 46.6 / 62.7 / 78.0 against 33.6 / 50.5 /
+// 67.9 / 77.5, int8 with its quantisation 16.3 / 28.3 / 37.6 / 45.8 against
+// 24.6 / 39.0 / 43.8 / 50.0; one such expert, 1 / 2 / 4 rows 9.6 / 12.4 / 17.8
+// against 14.2 / 13.9 / 14.1; the tiny layer's 16 / 32 rows 5.0 / 6.7 against
+// 4.9 / 4.9.
+bool grouped_gemv_pays(const GroupedProblem& p) {
+  if (p.kind != kGgForward && p.kind != kGgInt8) return false;
+  return p.rows <= (p.kind == kGgInt8 ? 16 : 12) && p.rows <= 2 * (p.E < p.rows ? p.E : p.rows);
 }
 
 cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st) {

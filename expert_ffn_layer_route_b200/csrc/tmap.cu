@@ -36,8 +36,8 @@ uintptr_t current_ctx() {
   return reinterpret_cast<uintptr_t>(c);
 }
 
-static bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
-                   const uint64_t* strides, const uint32_t* box, bool swizzle128, int l2_promo) {
+bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, bool swizzle128, int l2_promo) {
   auto fn = get_encoder();
   if (!fn) return false;
   cuuint64_t gd[5], gs[4];
@@ -48,7 +48,7 @@ static bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base,
     es[i] = 1;
     if (i + 1 < rank) gs[i] = strides[i];
   }
-  CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx, es,
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   l2_promo == 0    ? CU_TENSOR_MAP_L2_PROMOTION_NONE
@@ -57,16 +57,6 @@ static bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base,
                                     : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
-}
-
-bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                    const uint32_t* box, bool swizzle128, int l2_promo) {
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box, swizzle128, l2_promo);
-}
-
-bool encode_tmap_typed(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
-                       const uint64_t* strides, const uint32_t* box) {
-  return encode(map, type, base, rank, dims, strides, box, true, 256);
 }
 
 }  // namespace moe
