@@ -33,7 +33,7 @@ constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction ro
 constexpr int kABlock = kChan * kLine;  // the channels' operand of a block, either way
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 4;
-constexpr int kGgThreads = 32 * (2 + kEpiWarps);
+constexpr int gg_threads(int kind) { return 32 * (2 + kEpiWarps + (kind == kGgGradW ? 1 : 0)); }
 constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of the ragged operand
 
 // Staging buffer of one epilogue warp: 32 rows x 32 channels (forward, grad_x,
@@ -170,30 +170,89 @@ __device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, int n, 
   }
 }
 
-// One row's staged bytes to global memory in pieces of `vec` bytes, the pieces
-// of 32 lanes side by side; rows [0, n), bytes [0, width) of each.
+// The same for whatever does not fit that: results that lie on kVec bytes only,
+// edges (bytes [0, width) of each row), and (kAdd, fp32) sums added to what is
+// there.  Rows of kRowBytes, at(row, byte): the staged address.
 template <int kVec>
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const uint8_t* staged, int staged_pitch,
-                                           int row_bytes, int n, int width, int elem, int lane) {
-  const int shift = 31 - __clz(row_bytes / kVec);
-  for (int i = lane; i < (n << shift); i += 32) {
-    const int j = i >> shift, b = (i - (j << shift)) * kVec;
-    uint8_t* d = out + j * pitch + b;
-    const uint8_t* s = staged + j * staged_pitch + b;
-    if (b + kVec <= width) {
-      if constexpr (kVec == 16) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
-      if constexpr (kVec == 8) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
-      if constexpr (kVec == 4) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
-      if constexpr (kVec == 2) *reinterpret_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(s);
-    } else {
-      for (int z = 0; b + z < width; z += elem) {
-        if (elem == 4)
-          *reinterpret_cast<uint32_t*>(d + z) = *reinterpret_cast<const uint32_t*>(s + z);
-        else
-          *reinterpret_cast<uint16_t*>(d + z) = *reinterpret_cast<const uint16_t*>(s + z);
+struct Piece;
+template <>
+struct Piece<16> {
+  using T = uint4;
+};
+template <>
+struct Piece<8> {
+  using T = uint2;
+};
+template <>
+struct Piece<4> {
+  using T = uint32_t;
+};
+template <>
+struct Piece<2> {
+  using T = uint16_t;
+};
+
+template <int kVec, int kRowBytes, bool kAdd, typename At>
+__device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, int n, int width, int lane, At at) {
+  using T = typename Piece<kVec>::T;
+  constexpr int kPieces = kRowBytes / kVec, kBatch = kPieces < 8 ? kPieces : 8;
+#pragma unroll 1
+  for (int i0 = 0; i0 * 32 < n * kPieces; i0 += kBatch) {
+    T t[kBatch];
+    float old[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at_i = (i0 + i) * 32 + lane, r = at_i / kPieces, b = (at_i % kPieces) * kVec;
+      t[i] = *reinterpret_cast<const T*>(at(r, b));
+      if (kAdd && r < n && b < width) old[i] = *reinterpret_cast<const float*>(out + r * pitch + b);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at_i = (i0 + i) * 32 + lane, r = at_i / kPieces, b = (at_i % kPieces) * kVec;
+      if (r >= n || b >= width) continue;
+      uint8_t* d = out + r * pitch + b;
+      if constexpr (kAdd) {
+        *reinterpret_cast<float*>(d) = old[i] + __uint_as_float(*reinterpret_cast<const uint32_t*>(&t[i]));
+      } else if (b + kVec <= width) {
+        *reinterpret_cast<T*>(d) = t[i];
+      } else {
+        for (int z = 0; b + z < width; z += 2)
+          *reinterpret_cast<uint16_t*>(d + z) = *reinterpret_cast<const uint16_t*>(at(r, b + z));
       }
     }
   }
+}
+
+// (out of line, both: the common case must stay small)
+// rows of 32 channels, kElem bytes each
+template <int kElem>
+__device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, const uint8_t* staged, int n, int width, int vec,
+                                            int lane) {
+  auto at = [&](int r, int b) { return staged + r * (kElem == 4 ? kPitch32 : kPitch16) + b; };
+  if (vec == 16)
+    store_pieces<16, 32 * kElem, false>(out, pitch, n, width, lane, at);
+  else if (vec == 8)
+    store_pieces<8, 32 * kElem, false>(out, pitch, n, width, lane, at);
+  else if (vec == 4 || kElem == 4)
+    store_pieces<4, 32 * kElem, false>(out, pitch, n, width, lane, at);
+  else
+    store_pieces<2, 32 * kElem, false>(out, pitch, n, width, lane, at);
+}
+
+// lines of 128 bytes, their 16-byte pieces swizzled
+__device__ __noinline__ void store_lines_any(uint8_t* out, int64_t pitch, const uint8_t* staged, int n, int width,
+                                             int vec, int add, int lane) {
+  auto at = [&](int r, int b) { return staged + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15); };
+  if (add)
+    store_pieces<4, 128, true>(out, pitch, n, width, lane, at);
+  else if (vec == 16)
+    store_pieces<16, 128, false>(out, pitch, n, width, lane, at);
+  else if (vec == 8)
+    store_pieces<8, 128, false>(out, pitch, n, width, lane, at);
+  else if (vec == 4)
+    store_pieces<4, 128, false>(out, pitch, n, width, lane, at);
+  else
+    store_pieces<2, 128, false>(out, pitch, n, width, lane, at);
 }
 
 }  // namespace
@@ -203,7 +262,7 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const ui
 // even CTA issues one MMA for both, and each keeps its 128 channels of D.  Each
 // operand byte then crosses L2 -> SM half as often as with tiles of one CTA.
 template <int kKind, bool kPair>
-__global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __grid_constant__ GgArgs a) {
+__global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(const __grid_constant__ GgArgs a) {
   constexpr bool kAChanMajor = kKind == kGgGradX || kKind == kGgGradW;  // A rows run along the channels
   constexpr bool kBChanMajor = kKind == kGgGradW;
   constexpr int kElem = kKind == kGgInt8 ? 1 : 2;
@@ -224,9 +283,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   uint8_t* epi = ring + (size_t)a.stages * a.stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(epi + kEpiWarps * kEpiBytes);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* tail = empty + kMaxStages;  // grad_w: this CTA's half of a group's last stage has landed
-  uint64_t* peer = tail + kMaxStages;   // grad_w: the odd CTA has cleared its half of it
-  uint64_t* acc_full = peer + kMaxStages;
+  uint64_t* tail = empty + kMaxStages;  // grad_w: this CTA's half of a group's ragged last stage has landed
+  uint64_t* acc_full = tail + kMaxStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -236,10 +294,10 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
 
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&full[i], 1);
+      // (grad_w: two arrivals, as a ragged stage is handed over by each CTA's clearing warp)
+      mbar_init(&full[i], kKind == kGgGradW ? 2 : 1);
       mbar_init(&empty[i], 1);
       mbar_init(&tail[i], 1);
-      mbar_init(&peer[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -253,7 +311,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
   pdl_wait_and_trigger();
   // Group table.  Every thread loads the offsets of some experts (one round of
   // global latency for all of them), then warp 0 compacts and numbers them.
-  for (int e = tid; e < a.E; e += kGgThreads) {
+  for (int e = tid; e < a.E; e += gg_threads(kKind)) {
     const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
     int n = hi - lo, p = e;
     if (lo < 0 || hi < lo || hi > a.rows) {
@@ -372,9 +430,9 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
           // the pair's copies are counted together on the even CTA's barrier (a ragged stage's on each CTA's own)
           if (rag) {
             mbar_arrive_expect_tx(bar, bytes);
-            if (rank == 0) mbar_arrive(&full[s]);
           } else if (rank == 0) {
             mbar_arrive_expect_tx(bar, kPair ? 2 * bytes : bytes);
+            if (kKind == kGgGradW) mbar_arrive(bar);
           }
           const uint32_t bar_pair = kPair ? cluster_addr(bar, rag ? rank : 0) : 0;
           auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
@@ -425,82 +483,57 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
     }
   } else if (warp == 1) {
     // ================================================================ MMA issuer
-    // (The odd CTA of a pair only clears its half of the ragged stages.)
-    uint32_t s = 0, par = 0, tail_par = 0;
+    // (of the even CTA)
+    uint32_t s = 0, par = 0;
     int i = 0;
     const uint32_t sa0 = smem_u32(ring), sb0 = sa0 + a.blocks * kABlock;
     const uint64_t a_desc0 = kAChanMajor ? tc::mnmajor_sw128_desc(sa0, kSlabBytes) : tc::kmajor_sw128_desc(sa0);
     const uint64_t b_desc0 = kBChanMajor ? tc::mnmajor_sw128_desc(sb0, kSlabBytes) : tc::kmajor_sw128_desc(sb0);
-    for (int t = unit; t < total_tiles; t += units, ++i) {
+    for (int t = unit; t < total_tiles && rank == 0; t += units, ++i) {
       const Tile ti = tile_at(t);
       const int depth = uni(depth_of(ti));
       const int ncols = uni(mma_cols(ti));
-      const int bc = kPair ? ncols >> 1 : ncols;
       const int buf = i & 1;
-      if (kKind != kGgGradW && rank != 0) break;
-      if (rank == 0) {
-        if (*s_abort || !mbar_wait<kPair>(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+      if (*s_abort || !mbar_wait<kPair>(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+        *s_abort = 1;
+        break;
+      }
+      tc::fence_after_sync();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * a.col_cap);
+      const uint32_t idesc = a.idesc | ((uint32_t)(ncols >> 3) << 17);
+      for (int d0 = 0; d0 < depth; d0 += step_depth) {
+        const int left = depth - d0;
+        if (!mbar_wait<kPair>(&full[s], par)) {
           *s_abort = 1;
           break;
         }
         tc::fence_after_sync();
-      }
-      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * a.col_cap);
-      const uint32_t idesc = a.idesc | ((uint32_t)(ncols >> 3) << 17);
-      for (int d0 = 0; d0 < depth; d0 += step_depth) {
-        uint8_t* st = ring + (size_t)s * a.stage_bytes;
-        const int left = depth - d0;
-        if (rank == 0 && !mbar_wait<kPair>(&full[s], par)) {
-          *s_abort = 1;
-          break;
-        }
-        if (ragged(left)) {
-          if (!mbar_wait(&tail[s], (tail_par >> s) & 1u)) {
-            *s_abort = 1;
-            break;
-          }
-          clear_tail(st, left, 2, lane);
-          clear_tail(st + kABlock, left, ceil_div(bc, 64), lane);
-          if (kPair) {
-            if (rank != 0) {
-              if (lane == 0) mbar_arrive_cluster(cluster_addr(&peer[s], 0));
-            } else if (!mbar_wait<true>(&peer[s], (tail_par >> s) & 1u)) {
-              *s_abort = 1;
-              break;
-            }
-          }
-          tail_par ^= 1u << s;
-        }
-        if (rank == 0) {
-          tc::fence_after_sync();
-          // Descriptors count in 16 bytes: the next MMA's operands lie 32 bytes (K-major) or 16 lines
-          // (channel-major) on, the next block's a_block and b_block.  The whole warp runs this loop and
-          // one lane is elected at the instructions: with values the compiler knows to be the same in all
-          // lanes it keeps them in uniform registers, where the MMA wants them.
-          constexpr int kStepA = kAChanMajor ? 128 : 2, kStepB = kBChanMajor ? 128 : 2;
-          uint64_t da = a_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
-          uint64_t db = b_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
-          uint32_t more = d0 != 0;
-          for (int l = left; l > 0 && l > left - step_depth; l -= kDepthBlock) {
-            if (l >= kDepthBlock) {
-              if (tc::elect_one()) {
+        // Descriptors count in 16 bytes: the next MMA's operands lie 32 bytes (K-major) or 16 lines
+        // (channel-major) on, the next block's kABlock and b_block.  The whole warp runs this loop and
+        // one lane is elected at the instructions: with values the compiler knows to be the same in all
+        // lanes it keeps them in uniform registers, where the MMA wants them.
+        constexpr int kStepA = kAChanMajor ? 128 : 2, kStepB = kBChanMajor ? 128 : 2;
+        uint64_t da = a_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
+        uint64_t db = b_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
+        uint32_t more = d0 != 0;
+        for (int l = left; l > 0 && l > left - step_depth; l -= kDepthBlock) {
+          if (l >= kDepthBlock) {
+            if (tc::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  tc::mma_g<kPair, kKind == kGgInt8>(d_tmem, da + kk * kStepA, db + kk * kStepB, idesc,
-                                                     kk == 0 ? more : 1u);
-              }
-            } else {
-              for (int kk = 0; kk * kDepthMma < l; ++kk)
-                if (tc::elect_one())
-                  tc::mma_g<kPair, kKind == kGgInt8>(d_tmem, da + kk * kStepA, db + kk * kStepB, idesc,
-                                                     kk == 0 ? more : 1u);
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_g<kPair, kKind == kGgInt8>(d_tmem, da + kk * kStepA, db + kk * kStepB, idesc,
+                                                   kk == 0 ? more : 1u);
             }
-            more = 1;
-            da += kABlock >> 4;
-            db += (uint32_t)a.b_block >> 4;
+          } else if (tc::elect_one()) {
+            for (int kk = 0; kk * kDepthMma < l; ++kk)
+              tc::mma_g<kPair, kKind == kGgInt8>(d_tmem, da + kk * kStepA, db + kk * kStepB, idesc,
+                                                 kk == 0 ? more : 1u);
           }
-          if (tc::elect_one()) tc::commit_g<kPair>(&empty[s]);  // frees the stage once these MMAs have read it
+          more = 1;
+          da += kABlock >> 4;
+          db += (uint32_t)a.b_block >> 4;
         }
+        if (tc::elect_one()) tc::commit_g<kPair>(&empty[s]);  // frees the stage once these MMAs have read it
         __syncwarp();
         if (++s == (uint32_t)a.stages) {
           s = 0;
@@ -508,7 +541,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
         }
       }
       if (*s_abort) break;
-      if (rank == 0 && tc::elect_one()) tc::commit_g<kPair>(&acc_full[buf]);  // (an empty group: at once)
+      if (tc::elect_one()) tc::commit_g<kPair>(&acc_full[buf]);  // (an empty group: at once)
       __syncwarp();
     }
     if (rank == 0) {  // every MMA has completed before TMEM is freed
@@ -516,7 +549,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
       mbar_wait(drain, 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 2 + kEpiWarps) {
     // ================================================================ epilogue
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     uint8_t* stage_o = epi + (warp - 2) * kEpiBytes;
@@ -568,70 +601,23 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
             }
           }
           __syncwarp();
-          if (j0 + per_line < ti.nc) {  // the next line's values come while this one's leave
+          const int width = min(128, (ti.nc - j0) * osz);
+          const bool wide = a.vec == 16 && width == 128 && !a.accumulate;
+          // the next line's values come while this one's leave (not across a call: they arrive in registers)
+          auto issue_next = [&] {
+            if (j0 + per_line >= ti.nc) return;
             tc::ld_issue32(taddr + j0 + per_line, v);
             if (osz == 2) tc::ld_issue32(taddr + j0 + per_line + 32, v2);
-          }
-          const int width = min(128, (ti.nc - j0) * osz);
-          if (a.vec == 16 && width == 128 && !a.accumulate) {
+          };
+          if (wide) {
+            issue_next();
             const uint32_t base = smem_u32(stage_o);
             store_lines<8>(o + j0 * osz, op, n, lane,
                            [&](int r, int p) { return base + r * 128 + ((p ^ (r & 7)) << 4); });
-          } else if (a.vec == 16) {
-            const int piece = lane & 7, r0 = lane >> 3;
-            uint8_t* d = o + j0 * osz + r0 * op + piece * 16;
-            const bool whole = piece * 16 + 16 <= width;
-            if (a.accumulate) {
-#pragma unroll
-              for (int r = 0; r < 32; r += 4) {
-                float4 f = *reinterpret_cast<const float4*>(stage_o + (r0 + r) * 128 + ((piece ^ ((r0 + r) & 7)) << 4));
-                float* g = reinterpret_cast<float*>(d + r * op);
-                if (r0 + r < n) {
-                  if (whole) {
-                    const float4 h = *reinterpret_cast<const float4*>(g);
-                    *reinterpret_cast<float4*>(g) = make_float4(h.x + f.x, h.y + f.y, h.z + f.z, h.w + f.w);
-                  } else {
-                    const float e[4] = {f.x, f.y, f.z, f.w};
-                    for (int z = 0; z < 4; ++z)
-                      if (piece * 16 + z * 4 < width) g[z] += e[z];
-                  }
-                }
-              }
-            } else {
-#pragma unroll
-              for (int r = 0; r < 32; r += 4) {
-                const uint8_t* sp = stage_o + (r0 + r) * 128 + ((piece ^ ((r0 + r) & 7)) << 4);
-                if (r0 + r < n) {
-                  if (whole)
-                    *reinterpret_cast<uint4*>(d + r * op) = *reinterpret_cast<const uint4*>(sp);
-                  else
-                    for (int z = 0; piece * 16 + z < width; z += osz) {
-                      if (osz == 4)
-                        *reinterpret_cast<uint32_t*>(d + r * op + z) = *reinterpret_cast<const uint32_t*>(sp + z);
-                      else
-                        *reinterpret_cast<uint16_t*>(d + r * op + z) = *reinterpret_cast<const uint16_t*>(sp + z);
-                    }
-                }
-              }
-            }
           } else {
-            // rows that do not start on 16 bytes: a line at a time, 4 bytes a lane
-            uint8_t* d = o + j0 * osz + lane * 4;
-#pragma unroll 4
-            for (int r = 0; r < n; ++r, d += op) {
-              const uint32_t word = *reinterpret_cast<const uint32_t*>(
-                  stage_o + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
-              if (osz == 4) {
-                float* g = reinterpret_cast<float*>(d);
-                if (lane * 4 < width) *g = a.accumulate ? *g + __uint_as_float(word) : __uint_as_float(word);
-              } else if (a.vec >= 4 && lane * 4 + 4 <= width) {
-                *reinterpret_cast<uint32_t*>(d) = word;
-              } else {
-                uint16_t* g = reinterpret_cast<uint16_t*>(d);
-                if (lane * 4 < width) g[0] = (uint16_t)word;
-                if (lane * 4 + 2 < width) g[1] = (uint16_t)(word >> 16);
-              }
-            }
+            store_lines_any(o + j0 * osz, op, stage_o, n, width, a.vec, a.accumulate, lane);
+            __syncwarp();
+            issue_next();
           }
           __syncwarp();
         }
@@ -642,7 +628,6 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
         if (kKind == kGgInt8 && ch0 + lane < a.channels)
           sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
         const int64_t row0 = (int64_t)ti.row0 + ti.c0;
-        const int pitch = osz == 4 ? kPitch32 : kPitch16;
         const int width = min(32, a.channels - ch0) * osz;
         uint32_t v[32];
         tc::ld_issue32(taddr, v);
@@ -665,22 +650,25 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
             }
           }
           __syncwarp();
-          if (j0 + 32 < ti.nc) tc::ld_issue32(taddr + j0 + 32, v);  // comes while these rows leave
+          // the next rows' values come while these leave (not across a call: they arrive in registers)
+          const bool next = j0 + 32 < ti.nc;
+          const bool wide = a.vec == 16 && width == 32 * osz;
+          if (next && wide) tc::ld_issue32(taddr + j0 + 32, v);
           uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
           const int64_t op = a.ldo * osz;
           const uint32_t base = smem_u32(stage_o);
-          if (a.vec == 16 && width == 128)
+          if (!wide) {
+            if (osz == 4)
+              store_rows_any<4>(o, op, stage_o, n, width, a.vec, lane);
+            else
+              store_rows_any<2>(o, op, stage_o, n, width, a.vec, lane);
+            __syncwarp();
+            if (next) tc::ld_issue32(taddr + j0 + 32, v);
+          } else if (osz == 4) {
             store_lines<8>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch32 + p * 16; });
-          else if (a.vec == 16 && osz == 2 && width == 64)
+          } else {
             store_lines<4>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch16 + p * 16; });
-          else if (a.vec == 16)
-            store_rows<16>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
-          else if (a.vec == 8)
-            store_rows<8>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
-          else if (a.vec == 4)
-            store_rows<4>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
-          else
-            store_rows<2>(o, op, stage_o, pitch, 32 * osz, n, width, osz, lane);
+          }
           __syncwarp();
         }
       }
@@ -692,6 +680,24 @@ __global__ void __launch_bounds__(kGgThreads, 1) grouped_gemm_kernel(const __gri
         else
           mbar_arrive(&acc_empty[buf]);
       }
+    }
+  }
+  if (kKind == kGgGradW && warp == 2 + kEpiWarps) {
+    // ================================================================ clears the ragged stages
+    uint32_t cnt = 0, uses = 0;
+    for (int t = unit; t < total_tiles; t += units) {
+      const Tile ti = tile_at(t);
+      cnt += ceil_div(ti.n, kDepthBlock);
+      const int left = ti.n % kDepthBlock;
+      if ((left & 15) == 0) continue;
+      const uint32_t s = (cnt - 1) % a.stages;
+      if (*s_abort || !mbar_wait(&tail[s], (uses >> s) & 1u)) {
+        *s_abort = 1;
+        break;
+      }
+      uses ^= 1u << s;
+      clear_tail(ring + s * (uint32_t)a.stage_bytes, left, 2 + ceil_div(mma_cols(ti) >> 1, 64), lane);
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[s], 0));
     }
   }
   __syncwarp();
@@ -715,7 +721,7 @@ cudaError_t launch_kind(const GgArgs& a, int grid, size_t smem, cudaStream_t st)
   ProfScope prof(names[kKind], st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kGgThreads);
+  cfg.blockDim = dim3(gg_threads(kKind));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
