@@ -170,54 +170,56 @@ __device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, int n, 
   }
 }
 
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[1]) { v[0] = lds32(addr); }
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[2]) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
+}
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[4]) {
+  const uint4 u = lds128(addr);
+  v[0] = u.x;
+  v[1] = u.y;
+  v[2] = u.z;
+  v[3] = u.w;
+}
+
 // The same for whatever does not fit that: results that lie on kVec bytes only,
 // edges (bytes [0, width) of each row), and (kAdd, fp32) sums added to what is
-// there.  Rows of kRowBytes, at(row, byte): the staged address.
-template <int kVec>
-struct Piece;
-template <>
-struct Piece<16> {
-  using T = uint4;
-};
-template <>
-struct Piece<8> {
-  using T = uint2;
-};
-template <>
-struct Piece<4> {
-  using T = uint32_t;
-};
-template <>
-struct Piece<2> {
-  using T = uint16_t;
-};
-
-template <int kVec, int kRowBytes, bool kAdd, typename At>
-__device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, int n, int width, int lane, At at) {
-  using T = typename Piece<kVec>::T;
-  constexpr int kPieces = kRowBytes / kVec, kBatch = kPieces < 8 ? kPieces : 8;
+// there.  Staged rows of kRowBytes, kPitch apart, their 16-byte pieces swizzled
+// or not; a lane keeps its place in the row and steps through the rows.
+template <int kVec, int kRowBytes, int kPitch, bool kSwizzled, bool kAdd>
+__device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int lane) {
+  constexpr int kBytes = kVec < 4 ? 4 : kVec, kWords = kBytes / 4;  // per lane and row
+  constexpr int kPieces = kRowBytes / kBytes, kRows = 32 / kPieces, kBatch = kPieces < 8 ? kPieces : 8;
+  const int r0 = lane / kPieces, b = lane % kPieces * kBytes;
+  const uint32_t s = staged + r0 * kPitch + (kSwizzled ? (((b >> 4) ^ r0) << 4 | (b & 15)) : b);
+  uint8_t* d = out + r0 * pitch + b;
+  const bool whole = b + kBytes <= width;
+  if (b >= width) return;
 #pragma unroll 1
-  for (int i0 = 0; i0 * 32 < n * kPieces; i0 += kBatch) {
-    T t[kBatch];
+  for (int i0 = 0; i0 * kRows < n; i0 += kBatch) {
+    uint32_t t[kBatch][kWords];
     float old[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int at_i = (i0 + i) * 32 + lane, r = at_i / kPieces, b = (at_i % kPieces) * kVec;
-      t[i] = *reinterpret_cast<const T*>(at(r, b));
-      if (kAdd && r < n && b < width) old[i] = *reinterpret_cast<const float*>(out + r * pitch + b);
+    for (int i = 0; i < kBatch; ++i) {  // (a batch is a multiple of 8 rows where the swizzle counts)
+      lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + (i0 + i) * kRows * kPitch, t[i]);
+      if (kAdd && r0 + (i0 + i) * kRows < n) old[i] = *reinterpret_cast<const float*>(d + i * kRows * pitch);
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int at_i = (i0 + i) * 32 + lane, r = at_i / kPieces, b = (at_i % kPieces) * kVec;
-      if (r >= n || b >= width) continue;
-      uint8_t* d = out + r * pitch + b;
+    for (int i = 0; i < kBatch; ++i, d += kRows * pitch) {
+      if (r0 + (i0 + i) * kRows >= n) continue;
       if constexpr (kAdd) {
-        *reinterpret_cast<float*>(d) = old[i] + __uint_as_float(*reinterpret_cast<const uint32_t*>(&t[i]));
-      } else if (b + kVec <= width) {
-        *reinterpret_cast<T*>(d) = t[i];
+        *reinterpret_cast<float*>(d) = old[i] + __uint_as_float(t[i][0]);
+      } else if (kVec >= 4 && whole) {
+        if constexpr (kWords == 4)
+          st_global16(d, make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]));
+        else if constexpr (kWords == 2)
+          *reinterpret_cast<uint2*>(d) = make_uint2(t[i][0], t[i][1]);
+        else
+          *reinterpret_cast<uint32_t*>(d) = t[i][0];
       } else {
-        for (int z = 0; b + z < width; z += 2)
-          *reinterpret_cast<uint16_t*>(d + z) = *reinterpret_cast<const uint16_t*>(at(r, b + z));
+#pragma unroll
+        for (int z = 0; z < kBytes; z += 2)
+          if (b + z < width) *reinterpret_cast<uint16_t*>(d + z) = (uint16_t)(t[i][z >> 2] >> (8 * (z & 2)));
       }
     }
   }
@@ -226,33 +228,32 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, int n,
 // (out of line, both: the common case must stay small)
 // rows of 32 channels, kElem bytes each
 template <int kElem>
-__device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, const uint8_t* staged, int n, int width, int vec,
+__device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
                                             int lane) {
-  auto at = [&](int r, int b) { return staged + r * (kElem == 4 ? kPitch32 : kPitch16) + b; };
+  constexpr int kRow = 32 * kElem, kStaged = kElem == 4 ? kPitch32 : kPitch16;
   if (vec == 16)
-    store_pieces<16, 32 * kElem, false>(out, pitch, n, width, lane, at);
+    store_pieces<16, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
   else if (vec == 8)
-    store_pieces<8, 32 * kElem, false>(out, pitch, n, width, lane, at);
+    store_pieces<8, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
   else if (vec == 4 || kElem == 4)
-    store_pieces<4, 32 * kElem, false>(out, pitch, n, width, lane, at);
+    store_pieces<4, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
   else
-    store_pieces<2, 32 * kElem, false>(out, pitch, n, width, lane, at);
+    store_pieces<2, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
 }
 
 // lines of 128 bytes, their 16-byte pieces swizzled
-__device__ __noinline__ void store_lines_any(uint8_t* out, int64_t pitch, const uint8_t* staged, int n, int width,
-                                             int vec, int add, int lane) {
-  auto at = [&](int r, int b) { return staged + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15); };
+__device__ __noinline__ void store_lines_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
+                                             int add, int lane) {
   if (add)
-    store_pieces<4, 128, true>(out, pitch, n, width, lane, at);
+    store_pieces<4, 128, 128, true, true>(out, pitch, staged, n, width, lane);
   else if (vec == 16)
-    store_pieces<16, 128, false>(out, pitch, n, width, lane, at);
+    store_pieces<16, 128, 128, true, false>(out, pitch, staged, n, width, lane);
   else if (vec == 8)
-    store_pieces<8, 128, false>(out, pitch, n, width, lane, at);
+    store_pieces<8, 128, 128, true, false>(out, pitch, staged, n, width, lane);
   else if (vec == 4)
-    store_pieces<4, 128, false>(out, pitch, n, width, lane, at);
+    store_pieces<4, 128, 128, true, false>(out, pitch, staged, n, width, lane);
   else
-    store_pieces<2, 128, false>(out, pitch, n, width, lane, at);
+    store_pieces<2, 128, 128, true, false>(out, pitch, staged, n, width, lane);
 }
 
 }  // namespace
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
             store_lines<8>(o + j0 * osz, op, n, lane,
                            [&](int r, int p) { return base + r * 128 + ((p ^ (r & 7)) << 4); });
           } else {
-            store_lines_any(o + j0 * osz, op, stage_o, n, width, a.vec, a.accumulate, lane);
+            store_lines_any(o + j0 * osz, op, smem_u32(stage_o), n, width, a.vec, a.accumulate, lane);
             __syncwarp();
             issue_next();
           }
@@ -659,9 +660,9 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
           const uint32_t base = smem_u32(stage_o);
           if (!wide) {
             if (osz == 4)
-              store_rows_any<4>(o, op, stage_o, n, width, a.vec, lane);
+              store_rows_any<4>(o, op, base, n, width, a.vec, lane);
             else
-              store_rows_any<2>(o, op, stage_o, n, width, a.vec, lane);
+              store_rows_any<2>(o, op, base, n, width, a.vec, lane);
             __syncwarp();
             if (next) tc::ld_issue32(taddr + j0 + 32, v);
           } else if (osz == 4) {
