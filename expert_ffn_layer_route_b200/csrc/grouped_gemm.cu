@@ -193,34 +193,51 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
   const int r0 = lane / kPieces, b = lane % kPieces * kBytes;
   const uint32_t s = staged + r0 * kPitch + (kSwizzled ? (((b >> 4) ^ r0) << 4 | (b & 15)) : b);
   uint8_t* d = out + r0 * pitch + b;
-  const bool whole = b + kBytes <= width;
-  if (b >= width) return;
-#pragma unroll 1
-  for (int i0 = 0; i0 * kRows < n; i0 += kBatch) {
-    uint32_t t[kBatch][kWords];
-    float old[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {  // (a batch is a multiple of 8 rows where the swizzle counts)
-      lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + (i0 + i) * kRows * kPitch, t[i]);
-      if (kAdd && r0 + (i0 + i) * kRows < n) old[i] = *reinterpret_cast<const float*>(d + i * kRows * pitch);
+  auto put = [&](uint8_t* p, const uint32_t(&t)[kWords], float old) {
+    if constexpr (kAdd)
+      *reinterpret_cast<float*>(p) = old + __uint_as_float(t[0]);
+    else if constexpr (kWords == 4)
+      st_global16(p, make_uint4(t[0], t[1], t[2], t[3]));
+    else if constexpr (kWords == 2)
+      *reinterpret_cast<uint2*>(p) = make_uint2(t[0], t[1]);
+    else if constexpr (kVec == 4)
+      *reinterpret_cast<uint32_t*>(p) = t[0];
+    else {
+      reinterpret_cast<uint16_t*>(p)[0] = (uint16_t)t[0];
+      reinterpret_cast<uint16_t*>(p)[1] = (uint16_t)(t[0] >> 16);
     }
+  };
+  if (b + kBytes <= width) {
+#pragma unroll 1
+    for (int i0 = 0; i0 * kRows < n; i0 += kBatch) {
+      uint32_t t[kBatch][kWords];
+      float old[kBatch];
+      uint8_t* p[kBatch];
+      const int left = n - r0 - i0 * kRows;  // rows from this lane's first on
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i, d += kRows * pitch) {
-      if (r0 + (i0 + i) * kRows >= n) continue;
-      if constexpr (kAdd) {
-        *reinterpret_cast<float*>(d) = old[i] + __uint_as_float(t[i][0]);
-      } else if (kVec >= 4 && whole) {
-        if constexpr (kWords == 4)
-          st_global16(d, make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]));
-        else if constexpr (kWords == 2)
-          *reinterpret_cast<uint2*>(d) = make_uint2(t[i][0], t[i][1]);
-        else
-          *reinterpret_cast<uint32_t*>(d) = t[i][0];
+      for (int i = 0; i < kBatch; ++i) {  // (a batch is a multiple of 8 rows where the swizzle counts)
+        lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + (i0 + i) * kRows * kPitch, t[i]);
+        p[i] = d;
+        d += kRows * pitch;
+        if (kAdd && i * kRows < left) old[i] = *reinterpret_cast<const float*>(p[i]);
+      }
+      if (left >= (kBatch - 1) * kRows + 1) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) put(p[i], t[i], old[i]);
       } else {
 #pragma unroll
-        for (int z = 0; z < kBytes; z += 2)
-          if (b + z < width) *reinterpret_cast<uint16_t*>(d + z) = (uint16_t)(t[i][z >> 2] >> (8 * (z & 2)));
+        for (int i = 0; i < kBatch; ++i)
+          if (i * kRows < left) put(p[i], t[i], old[i]);
       }
+    }
+  } else if (b < width) {  // the row's end inside a lane's piece
+#pragma unroll 1
+    for (int r = r0, i = 0; r < n; r += kRows, ++i, d += kRows * pitch) {
+      uint32_t t[kWords];
+      lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + i * kRows * kPitch, t);
+#pragma unroll
+      for (int z = 0; z < kBytes; z += 2)
+        if (b + z < width) *reinterpret_cast<uint16_t*>(d + z) = (uint16_t)(t[z >> 2] >> (8 * (z & 2)));
     }
   }
 }
