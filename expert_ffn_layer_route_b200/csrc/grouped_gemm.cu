@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       prefetch_tmap(&a.tm_b);
       if (!kBChanMajor) prefetch_tmap(&a.tm_b16);
     }
-    const uint64_t pol = l2_evict_normal_policy();
+    // Large groups read every operand tile several times, from pairs that run side by side (Mixtral-shaped
+    // gate/up in a long loop at the power limit: 1576 us, 1532 with evict_last; dx 1715, 1690)
+    const uint64_t pol = kPair ? l2_evict_last_policy() : l2_evict_normal_policy();
     uint32_t s = 0, par = 1, cnt = 0, tails = 0, tail_use = 0;
     for (int t = unit; t < total_tiles; t += units) {
       if (*s_abort) break;
