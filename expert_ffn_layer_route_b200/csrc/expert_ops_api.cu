@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMaxExtent = 1 << 20;   // N, K: byte coordinates of a row stay far below 2^31
 constexpr int kMaxDepthI8 = 131071;   // 128 * 128 * K < 2^31: the int32 sum cannot overflow
+constexpr int kMaxGradRows = 1 << 26;  // one tile sums a group's rows: far below the limit of a device-side wait
 constexpr int64_t kMaxPitch = (int64_t)1 << 36;  // elements: byte strides stay below the tensor maps' 2^40
 
 bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
@@ -128,6 +129,7 @@ moe_status moe_grouped_gemm_grad_w(const moe_gemm_desc* desc, const void* dy, co
   moe_status s = check_gemm(desc, false, &t);
   if (s != MOE_OK) return s;
   if (accumulate && desc->out_dtype != MOE_T_FP32) return MOE_ERR_INVALID_ARG;
+  if (desc->rows > kMaxGradRows) return MOE_ERR_UNSUPPORTED;
   if (!offsets || !dw || !on(dw, size_of(desc->out_dtype))) return MOE_ERR_INVALID_ARG;
   if (desc->rows > 0 && (!operand(dy, t.y, 2) || !operand(x, t.x, 2))) return MOE_ERR_INVALID_ARG;
   GroupedProblem p = problem(kGgGradW, *desc, t);

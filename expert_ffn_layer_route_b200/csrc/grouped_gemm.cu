@@ -120,6 +120,15 @@ struct Walk {
   }
 };
 
+// A whole warp's wait: every lane polls, and all leave with the same answer, so
+// that a wait that was given up cannot part lanes that the warp's next
+// instructions (elections, tensor-memory loads) need together.
+template <bool kCluster = false>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity));
+}
+__device__ __forceinline__ bool warp_any(int v) { return __any_sync(0xffffffffu, v); }
+
 // A value that is the same in all lanes, in a register the compiler knows to
 // be: what TMA and MMA instructions take their operands from.
 __device__ __forceinline__ int uni(int v) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)v); }
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
     const uint64_t pol = kPair ? l2_evict_last_policy() : l2_evict_normal_policy();
     uint32_t s = 0, par = 1, cnt = 0, tails = 0, tail_use = 0;
     for (int t = unit; t < total_tiles; t += units) {
-      if (*s_abort) break;
+      if (warp_any(*s_abort)) break;
       const Tile ti = tile_at(t);
       const int depth = uni(depth_of(ti));
       const int ncols = uni(mma_cols(ti));
@@ -430,7 +439,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       const int phys = uni(ti.phys);
       const int b_bytes = kBChanMajor ? ceil_div(bc, 64) * kSlabBytes : bc * kLine;
       for (int d0 = 0; d0 < depth; d0 += step_depth) {
-        if (!mbar_wait(&empty[s], par)) {
+        if (!warp_wait(&empty[s], par)) {
           *s_abort = 1;
           break;
         }
@@ -492,9 +501,9 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
     }
     // Before the block may leave, every copy has landed and every arrival at
     // this CTA's barriers has come: the last uses of the stages are free again.
-    bool fine = !*s_abort;
+    bool fine = !warp_any(*s_abort);
     const uint32_t first = cnt > (uint32_t)a.stages ? cnt - a.stages : 0;
-    for (uint32_t c = first; fine && c < cnt; ++c) fine = mbar_wait(&empty[c % a.stages], (c / a.stages) & 1u);
+    for (uint32_t c = first; fine && c < cnt; ++c) fine = warp_wait(&empty[c % a.stages], (c / a.stages) & 1u);
     if (!fine) {  // given up somewhere: the copies alone
       for (uint32_t c = first; rank == 0 && c < cnt; ++c)
         if (!mbar_wait(&full[c % a.stages], (c / a.stages) & 1u)) break;
@@ -514,7 +523,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       const int depth = uni(depth_of(ti));
       const int ncols = uni(mma_cols(ti));
       const int buf = i & 1;
-      if (*s_abort || !mbar_wait<kPair>(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+      if (warp_any(*s_abort) || !warp_wait<kPair>(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         *s_abort = 1;
         break;
       }
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       const uint32_t idesc = a.idesc | ((uint32_t)(ncols >> 3) << 17);
       for (int d0 = 0; d0 < depth; d0 += step_depth) {
         const int left = depth - d0;
-        if (!mbar_wait<kPair>(&full[s], par)) {
+        if (!warp_wait<kPair>(&full[s], par)) {
           *s_abort = 1;
           break;
         }
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
           par ^= 1;
         }
       }
-      if (*s_abort) break;
+      if (warp_any(*s_abort)) break;
       if (tc::elect_one()) tc::commit_g<kPair>(&acc_full[buf]);  // (an empty group: at once)
       __syncwarp();
     }
@@ -578,7 +587,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
     for (int t = unit; t < total_tiles; t += units, ++i) {
       const Tile ti = tile_at(t);
       const int buf = i & 1;
-      if (*s_abort || !mbar_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
+      if (warp_any(*s_abort) || !warp_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
         *s_abort = 1;
         break;
       }
@@ -711,7 +720,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       const int left = ti.n % kDepthBlock;
       if ((left & 15) == 0) continue;
       const uint32_t s = (cnt - 1) % a.stages;
-      if (*s_abort || !mbar_wait(&tail[s], (uses >> s) & 1u)) {
+      if (warp_any(*s_abort) || !warp_wait(&tail[s], (uses >> s) & 1u)) {
         *s_abort = 1;
         break;
       }

@@ -83,7 +83,7 @@ __device__ __forceinline__ void tmem_dealloc_g(uint32_t taddr, uint32_t ncols) {
     tmem_dealloc(taddr, ncols);
 }
 
-// True in one lane of a converged warp (always the same one).
+// True in one lane of a warp (always the same one); waits for all of its lanes.
 __device__ __forceinline__ bool elect_one() {
   uint32_t on;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));

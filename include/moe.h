@@ -238,8 +238,10 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, const vo
  * read into any result nor written.
  *
  * Values of each product are exact products summed in fp32 (int8: exactly, in
- * int32) and rounded once to the output type.  The result of a row depends on
- * no other row, and the same call gives the same bits again.  Groups may be
+ * int32) and rounded once to the output type.  A row's result is computed from
+ * that row alone, and the same call gives the same bits again; the order of the
+ * fp32 sum, and so its last bits, may change with the number of rows in the
+ * call.  Groups may be
  * empty, of one row, or all rows; nothing has to be a multiple of anything,
  * but the matrices that are read (w, x, dy, codes) need a base and a row pitch
  * of whole 16 bytes.  Outputs need only the alignment of their type; pitches
@@ -265,7 +267,8 @@ typedef struct {
 /* out[r][n] = sum_k x[r][k] * w[p][n][k], p = slot_map ? slot_map[e] : e.
  * x [rows][K], w [n_physical][N][K], out [rows][N].  slot_map: device int32
  * [E] or NULL; an entry of -1 skips the expert, any other entry outside
- * [0, n_physical) also sets MOE_ERR_DEVICE_INDEX. */
+ * [0, n_physical) also sets MOE_ERR_DEVICE_INDEX (entries of experts without
+ * rows are not looked at). */
 moe_status moe_grouped_gemm(const moe_gemm_desc* desc, const void* x, const void* w, const int32_t* slot_map,
                             const int32_t* offsets, void* out, void* stream);
 
@@ -278,7 +281,7 @@ moe_status moe_grouped_gemm_grad_x(const moe_gemm_desc* desc, const void* dy, co
  * dw[e][n][k] = sum_{r of e} dy[r][n] * x[r][k], zeros for an expert without
  * rows; with accumulate != 0 (fp32 only) the sum is added to what dw holds,
  * rounded once.  out_dtype is dw's.  rows = 0 is a call like any other (it
- * writes zeros). */
+ * writes zeros); more than 2^26 rows are MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_gemm_grad_w(const moe_gemm_desc* desc, const void* dy, const void* x,
                                    const int32_t* offsets, void* dw, int accumulate, void* stream);
 

@@ -62,6 +62,10 @@ def test_types():
         assert _grad_w(_desc(out_dtype=out), acc=1) == INVALID  # sums are accumulated in fp32 only
 
 
+def test_grad_w_rows_are_limited():
+    assert _grad_w(_desc(rows=(1 << 26) + 1)) == UNSUPPORTED
+
+
 def test_null_and_misaligned():
     d, q = _desc(), _desc(dtype=3)
     L = moe.lib()

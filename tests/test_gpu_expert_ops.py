@@ -406,6 +406,144 @@ def test_results_past_32_bit_offsets():
     assert bool((big[-2] == 0).all())
 
 
+# rows of each expert, N, K: a handful of rows, where a kernel of its own runs, and just past it
+FEW = [([1] * 4, 130, 264), ([0, 1, 0, 2, 0, 0, 1], 33, 17), ([2, 0, 1], 257, 1), ([1] * 12, 64, 2880),
+       ([1] * 13, 64, 2880), ([1] * 16, 40, 5000), ([1] * 17, 40, 5000), ([5, 1, 1, 1, 0, 0, 0, 0], 96, 520),
+       ([2], 100, 300), ([3], 100, 300), ([0] * 1023 + [1], 35, 1031)]
+
+
+@pytest.mark.parametrize("counts,N,K", FEW, ids=[f"{sum(c)}of{len(c)}" for c, _, _ in FEW])
+@pytest.mark.parametrize("first,behind", [(0, 0), (2, 3)])
+def test_few_rows(counts, N, K, first, behind):
+    """Pads and rows outside the groups hold NaN and garbage; slots are permuted."""
+    g = gen(21)
+    E, R = len(counts), first + sum(counts) + behind
+    off = offsets_of(counts, first)
+    inside = slice(first, first + sum(counts))
+    slots = torch.randperm(E, generator=torch.Generator().manual_seed(2)).to(torch.int32)
+    for t in (BF16, FP16):
+        x, w = normal((R, K), t, g), normal((E, N, K), t, g, 0.1)
+        for m in (x, w):  # behind the rows' ends
+            if m._base is not None and m._base.shape[-1] > K:
+                m._base[..., K:] = float("nan")
+        x[:first], x[first + sum(counts):] = float("nan"), float("inf")
+        for ot in (t, FP32):
+            out = torch.full((R, N), 7.0, dtype=ot, device=DEV)
+            moe.moe_grouped_gemm(x, w, off, out, slot_map=slots.to(DEV))
+            ok()
+            ref, mag = ref_forward(x, w[slots.long()], off)
+            check(out[inside], ref[inside], mag[inside] * (K + 2) * U)
+            assert bool((out[:first] == 7.0).all()) and bool((out[first + sum(counts):] == 7.0).all())
+    x, w = codes((R, K), g), codes((E, N, K), g)
+    for m in (x, w):
+        if m._base is not None and m._base.shape[-1] > K:
+            m._base[..., K:] = 99
+    sx, sw = torch.rand(R, device=DEV), torch.rand(E, N, device=DEV)
+    out = torch.full((R, N), 7.0, device=DEV)
+    moe.moe_grouped_gemm_i8(x, sx, w, sw, off, out, slot_map=slots.to(DEV))
+    ok()
+    e = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    ref = ref_forward(x, w[slots.long()], off)[0][inside]
+    ref = ref * sx[inside].double()[:, None] * sw[slots.long()][e.to(DEV)].double()
+    check(out[inside], ref, ref.abs() * 2.0 ** -22)
+
+
+def test_pads_of_every_operand_are_not_read():
+    """NaN behind the rows' ends and between the matrices reaches nothing, in every kernel."""
+    g = gen(22)
+    for counts, N, K in (([3, 40, 0, 9], 77, 53), ([300, 5], 150, 70)):
+        R, E = sum(counts), len(counts)
+        off = offsets_of(counts)
+        x, dy = normal((R, K), BF16, g, 1, 1), normal((R, N), BF16, g, 1, 1)
+        wide = normal((E, N + 3, K), BF16, g, 0.1, 1)
+        w = wide[:, :N]
+        for m, n in ((x, K), (dy, N), (wide, K)):
+            m._base[..., n:] = float("nan")
+        wide[:, N:] = float("inf")
+        out, dx = torch.empty(R, N, dtype=BF16, device=DEV), torch.empty(R, K, dtype=BF16, device=DEV)
+        dw = torch.empty(E, N, K, device=DEV)
+        moe.moe_grouped_gemm(x, w, off, out)
+        moe.moe_grouped_gemm_grad_x(dy, w, off, dx)
+        moe.moe_grouped_gemm_grad_w(dy, x, off, dw)
+        ok()
+        ref, mag = ref_forward(x, w, off)
+        check(out, ref, mag * (K + 2) * U)
+        ref, mag = ref_forward(dy, w.transpose(1, 2), off)
+        check(dx, ref, mag * (N + 2) * U)
+        ref, mag = ref_grad_w(dy, x, off)
+        check(dw, ref, mag * (max(counts) + 2) * U)
+
+
+@pytest.mark.parametrize("R", [3, 40])
+def test_no_group_at_all(R):
+    """Every group empty, or every expert away: nothing is written but grad_w's zeros."""
+    g = gen(23)
+    x, dy, w = normal((R, 64), BF16, g), normal((R, 96), BF16, g), normal((5, 96, 64), BF16, g)
+    q, wq, sx, sw = codes((R, 64), g), codes((5, 96, 64), g), torch.rand(R, device=DEV), torch.rand(5, 96, device=DEV)
+    away = torch.full((5,), -1, dtype=torch.int32, device=DEV)
+    for off, m in ((torch.zeros(6, dtype=torch.int32, device=DEV), None),
+                   (torch.full((6,), R, dtype=torch.int32, device=DEV), None), (offsets_of([R, 0, 0, 0, 0]), away)):
+        out, dx = torch.full((R, 96), 7.0, dtype=BF16, device=DEV), torch.full((R, 64), 7.0, dtype=BF16, device=DEV)
+        moe.moe_grouped_gemm(x, w, off, out, slot_map=m)
+        moe.moe_grouped_gemm_grad_x(dy, w, off, dx, slot_map=m)
+        moe.moe_grouped_gemm_i8(q, sx, wq, sw, off, out, slot_map=m)
+        ok()
+        assert bool((out == 7.0).all()) and bool((dx == 7.0).all())
+    dw = torch.full((5, 96, 64), 7.0, device=DEV)
+    moe.moe_grouped_gemm_grad_w(dy, x, torch.zeros(6, dtype=torch.int32, device=DEV), dw)
+    ok()
+    assert bool((dw == 0).all())
+    dw.fill_(7.0)
+    moe.moe_grouped_gemm_grad_w(dy, x, torch.zeros(6, dtype=torch.int32, device=DEV), dw, accumulate=True)
+    ok()
+    assert bool((dw == 7.0).all())
+
+
+@pytest.mark.parametrize("N,K", [(24, 40), (300, 264), (130, 67)])
+def test_many_small_tiles_and_wide_offsets_of_one_call(N, K):
+    """1024 experts, most of one to three rows, two with many."""
+    g = gen(24)
+    counts = [(i * 5) % 4 for i in range(1024)]
+    counts[3], counts[700] = 600, 259
+    off, R = offsets_of(counts), sum(counts)
+    x, w = normal((R, K), FP16, g), normal((1024, N, K), FP16, g, 0.1)
+    out = torch.empty(R, N, dtype=FP16, device=DEV)
+    moe.moe_grouped_gemm(x, w, off, out)
+    ok()
+    ref, mag = ref_forward(x, w, off)
+    check(out, ref, mag * (K + 2) * U)
+    dy, dw = normal((R, N), FP16, g), torch.empty(1024, N, K, dtype=FP16, device=DEV)
+    moe.moe_grouped_gemm_grad_w(dy, x, off, dw)
+    ok()
+    ref, mag = ref_grad_w(dy, x, off)
+    check(dw, ref, mag * 602 * U)
+
+
+def test_gradients_against_differences():
+    """One number of x and of w moved a little either way: the slope of sum(out * dy) is the gradient."""
+    g = gen(25)
+    counts, N, K = [5, 0, 33], 40, 24
+    off = offsets_of(counts)
+    x, dy, w = normal((38, K), BF16, g), normal((38, N), BF16, g), normal((3, N, K), BF16, g, 0.1)
+    dx, dw = torch.empty(38, K, device=DEV), torch.empty(3, N, K, device=DEV)
+    moe.moe_grouped_gemm_grad_x(dy, w, off, dx)
+    moe.moe_grouped_gemm_grad_w(dy, x, off, dw)
+    ok()
+
+    def loss(a, b):
+        return (ref_forward(a, b, off)[0] * dy.double()).sum().item()
+
+    xd, wd, step = x.double(), w.double(), 0.5  # the loss is linear in either: any step will do
+    for r, k in ((0, 0), (4, 23), (5, 7), (37, 11)):
+        e = torch.zeros_like(xd)
+        e[r, k] = step
+        assert abs((loss(xd + e, wd) - loss(xd - e, wd)) / (2 * step) - dx[r, k].item()) <= 1e-4
+    for n, i, k in ((0, 0, 0), (0, 39, 23), (2, 17, 5), (1, 3, 3)):
+        e = torch.zeros_like(wd)
+        e[n, i, k] = step
+        assert abs((loss(xd, wd + e) - loss(xd, wd - e)) / (2 * step) - dw[n, i, k].item()) <= 1e-3
+
+
 # ------------------------------------------------------------- row operators
 
 def ref_codes(v):
