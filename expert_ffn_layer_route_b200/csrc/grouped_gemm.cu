@@ -32,8 +32,13 @@ constexpr int kLine = 128;             // bytes of the contraction per K-major b
 constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction rows x 64 channels of 16 bits
 constexpr int kABlock = kChan * kLine;  // the channels' operand of a block, either way
 constexpr int kMaxStages = 12;
-constexpr int kEpiWarps = 4;
-constexpr int gg_threads(int kind) { return 32 * (2 + kEpiWarps + (kind == kGgGradW ? 1 : 0)); }
+// A warp reads the 32 TMEM lanes of its quadrant.  grad_w has two warps to a
+// quadrant, which take its 128-byte columns in turn: with few rows to a group
+// its tiles are all epilogue, and a warp spends most of a column's 600 cycles on
+// latencies (fp32 gradients of 128 experts with 64 rows each: 868 us with 4
+// warps, 793 with 8).
+constexpr int epi_warps(int kind) { return kind == kGgGradW ? 8 : 4; }
+constexpr int gg_threads(int kind) { return 32 * (2 + epi_warps(kind) + (kind == kGgGradW ? 1 : 0)); }
 constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of the ragged operand
 
 // Staging buffer of one epilogue warp: 32 rows x 32 channels (forward, grad_x,
@@ -251,8 +256,7 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
   }
 }
 
-// (out of line, both: the common case must stay small)
-// rows of 32 channels, kElem bytes each
+// rows of 32 channels, kElem bytes each (out of line: the common case stays small)
 template <int kElem>
 __device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
                                             int lane) {
@@ -267,8 +271,9 @@ __device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, uint32_
     store_pieces<2, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
 }
 
-// lines of 128 bytes, their 16-byte pieces swizzled
-__device__ __noinline__ void store_lines_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
+// lines of 128 bytes, their 16-byte pieces swizzled (in line: a call here would have to save the columns that
+// are on their way from tensor memory)
+__device__ __forceinline__ void store_lines_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
                                              int add, int lane) {
   if (add)
     store_pieces<4, 128, 128, true, true>(out, pitch, staged, n, width, lane);
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
   constexpr int kDepthBlock = kLine / kElem;  // contraction elements per block
   constexpr int kDepthMma = 32 / kElem;
   constexpr int kColRound = kPair ? 32 : 16;
-  constexpr int kEpiBytes = epi_bytes(kKind);
+  constexpr int kEpiBytes = epi_bytes(kKind), kEpiWarps = epi_warps(kKind);
   constexpr int kTileChan = kPair ? 2 * kChan : kChan;
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -604,10 +609,10 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
                            ((int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0) * osz;
         const int64_t op = a.ldo * osz;
         const int n = min(32, a.channels - ch0);
-        uint32_t v[32], v2[32];
-        tc::ld_issue32(taddr, v);
-        if (osz == 2) tc::ld_issue32(taddr + 32, v2);
-        for (int j0 = 0; j0 < ti.nc; j0 += per_line) {
+        const int first = (warp - 2) / 4 * per_line, step = 2 * per_line;
+        uint32_t v[32];
+        if (first < ti.nc) tc::ld_issue32(taddr + first, v);
+        for (int j0 = first; j0 < ti.nc; j0 += step) {
           tc::ld_wait32(v);
           uint4* line = reinterpret_cast<uint4*>(stage_o + lane * 128);
           if (ti.n == 0) {
@@ -618,25 +623,25 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
             for (int c = 0; c < 8; ++c)
               line[c ^ (lane & 7)] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
           } else {
-            tc::ld_wait32(v2);
-            auto two = [&](const uint32_t(&u)[32], int j) {
-              return pack16(a.out_dtype, __uint_as_float(u[j]), __uint_as_float(u[j + 1]));
-            };
+            auto half_line = [&](int c0) {
+              auto two = [&](int j) {
+                return pack16(a.out_dtype, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+              };
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              line[c ^ (lane & 7)] = make_uint4(two(v, 8 * c), two(v, 8 * c + 2), two(v, 8 * c + 4), two(v, 8 * c + 6));
-              line[(c + 4) ^ (lane & 7)] =
-                  make_uint4(two(v2, 8 * c), two(v2, 8 * c + 2), two(v2, 8 * c + 4), two(v2, 8 * c + 6));
-            }
+              for (int c = 0; c < 4; ++c)
+                line[(c0 + c) ^ (lane & 7)] = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+            };
+            half_line(0);
+            tc::ld_issue32(taddr + j0 + 32, v);
+            tc::ld_wait32(v);
+            half_line(4);
           }
           __syncwarp();
           const int width = min(128, (ti.nc - j0) * osz);
           const bool wide = a.vec == 16 && width == 128 && !a.accumulate;
           // the next line's values come while this one's leave (not across a call: they arrive in registers)
           auto issue_next = [&] {
-            if (j0 + per_line >= ti.nc) return;
-            tc::ld_issue32(taddr + j0 + per_line, v);
-            if (osz == 2) tc::ld_issue32(taddr + j0 + per_line + 32, v2);
+            if (j0 + step < ti.nc) tc::ld_issue32(taddr + j0 + step, v);
           };
           if (wide) {
             issue_next();
@@ -815,7 +820,7 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   a.stage_bytes = a.blocks * (kABlock + a.b_block);
   a.tmem_cols = cap < 32 ? 64 : 2 * cap;  // (the epilogue reads 32 columns at a time)
   const size_t table = (size_t)(p.E + 1) * sizeof(Group);
-  const size_t fixed_bytes = 1024 + kEpiWarps * epi_bytes(p.kind) + (4 * kMaxStages + 8) * 8 + 32 + table;
+  const size_t fixed_bytes = 1024 + epi_warps(p.kind) * epi_bytes(p.kind) + (4 * kMaxStages + 8) * 8 + 32 + table;
   int stages = (int)(((size_t)smem_max - fixed_bytes) / a.stage_bytes);
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) {
