@@ -7,8 +7,8 @@
 //   codes of a row v: amax = max|v|, scale = amax / 127, inv = 127 / amax (two
 //   fp32 divisions), q = round-to-nearest-even(v inv) clamped to +-127
 // All sums, products and statistics are fp32.  Every value is read once and
-// written once: these kernels are bound by HBM (SwiGLU at fp32-exp rates of 16
-// per SM and cycle stays below it).
+// written once: these kernels are bound by HBM (8192 x 14336: SwiGLU 110 us, its
+// gradient 167 us, 6.4 and 7.0 TB/s), the int8 rows by the latencies of a row.
 #include "expert_rows.cuh"
 
 #include <type_traits>
