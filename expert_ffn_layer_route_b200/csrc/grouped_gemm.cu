@@ -42,6 +42,7 @@ constexpr int kLine = 128;             // bytes of the contraction per K-major b
 constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction rows x 64 channels of 16 bits
 constexpr int kABlock = kChan * kLine;  // the channels' operand of a block, either way
 constexpr int kMaxStages = 12;
+constexpr int64_t kMaxTiles = (int64_t)1 << 30;
 // A warp reads the 32 TMEM lanes of its quadrant.  grad_w has two warps to a
 // quadrant, which take its 128-byte columns in turn: with few rows to a group
 // its tiles are all epilogue, and a warp spends most of a column's 600 cycles on
@@ -386,16 +387,21 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
         ct = kKind != kGgGradW ? ceil_div(n, a.col_cap) : n == 0 && a.accumulate ? 0 : ceil_div(a.cols, a.col_cap);
         t = m_tiles * ct;
       }
-      const uint32_t on = __ballot_sync(0xffffffffu, t > 0);
-      int incl = t;
+      int64_t end = t;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
+        const int64_t o = __shfl_up_sync(0xffffffffu, end, off);
+        if (lane >= off) end += o;
       }
+      end += tiles;
+      if (t > 0 && end > kMaxTiles) {  // more tiles than rows allow: offsets that go back and forth
+        set_status(MOE_ERR_DEVICE_INDEX);
+        t = 0;
+      }
+      const uint32_t on = __ballot_sync(0xffffffffu, t > 0);
       if (t > 0) {  // slots at or before this expert's own: already read above
         Group g;
-        g.tile0 = tiles + incl - t;
+        g.tile0 = (int)end - t;
         g.ct = ct;
         g.w = ceil_div(ceil_div(kKind == kGgGradW ? a.cols : n, ct), a.col_step) * a.col_step;  // as even as the step allows
         g.per_ct = 1.f / (float)ct;
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
         grp[ng + __popc(on & ((1u << lane) - 1u))] = g;
       }
       ng += __popc(on);
-      tiles += __shfl_sync(0xffffffffu, incl, 31);
+      tiles = (int)__reduce_max_sync(0xffffffffu, (unsigned)(t > 0 ? (int)end : tiles));
       __syncwarp();
     }
     if (lane == 0) {
@@ -831,12 +837,12 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   a.col_step = gw ? 64 : pair ? 32 : 16;
   const int64_t col_tiles = gw ? p.E * div_up(p.K, cap) : groups + p.rows / cap;
   a.blocks = pair ? 1 : 2;
-    a.b_block = (pair ? cap / 2 : cap) * kLine;
+  a.b_block = (pair ? cap / 2 : cap) * kLine;
   a.stage_bytes = a.blocks * (kABlock + a.b_block);
   a.tmem_cols = cap < 32 ? 64 : 2 * cap;  // (the epilogue reads 32 columns at a time)
   const size_t table = (size_t)(p.E + 1) * sizeof(Group);
   const size_t fixed_bytes = 1024 + epi_warps(p.kind) * epi_bytes(p.kind) + (4 * kMaxStages + 8) * 8 + 32 + table;
-  int stages = (int)(((size_t)smem_max - fixed_bytes) / a.stage_bytes);
+  int stages = (smem_max - (int)fixed_bytes) / a.stage_bytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) {
     *unsupported = 1;
@@ -866,7 +872,7 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
          encode_tmap_u8(&a.tm_b16, p.b, 2, db, sb, box_b16, true);
   }
   const int64_t max_tiles = div_up(a.channels, pair ? 2 * kChan : kChan) * col_tiles;
-  if (!ok || max_tiles > (int64_t)1 << 30) {
+  if (!ok || max_tiles > kMaxTiles) {
     *unsupported = 1;
     return cudaSuccess;
   }

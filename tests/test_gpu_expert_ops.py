@@ -338,6 +338,22 @@ def test_bad_offsets_are_reported_and_skipped():
     ok()
 
 
+@pytest.mark.parametrize("R", [10, 300])
+def test_offsets_that_go_back_and_forth(R):
+    """Groups that claim the same rows: reported; every row gets the product of one of the experts, whole."""
+    g = gen(26)
+    E, N, K = 64, 96, 72
+    off = torch.tensor([0, R - 3] * (E // 2) + [0], dtype=torch.int32, device=DEV)
+    x = normal((R, K), BF16, g)
+    w = normal((1, N, K), BF16, g, 0.1).expand(E, N, K).contiguous()
+    out = torch.full((R, N), 7.0, dtype=BF16, device=DEV)
+    moe.moe_grouped_gemm(x, w, off, out)
+    assert moe.moe_get_last_error() == 9
+    ref, mag = ref_forward(x, w, offsets_of([R - 3] + [0] * (E - 1)))
+    check(out[: R - 3], ref[: R - 3], mag[: R - 3] * (K + 2) * U)
+    assert bool((out[R - 3:] == 7.0).all())
+
+
 @pytest.mark.parametrize("K", [40, 41])
 def test_grad_w_accumulates(K):
     g = gen(10)
