@@ -19,9 +19,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kGvThreads = 256;
-constexpr int kGvMinBlocks = 3;  // 24 warps and 85 registers a thread: 2 / 4 / 5 blocks were 28.7 / 29.6 / 25.6 us
-                                 // for one token (3: 25.8), 26.4 / 25.5 / 26.1 us in int8 (25.6)
+// 24 warps of 85 registers on an SM.  gpt-oss-shaped gate/up, one token / two
+// tokens in bf16, in int8 with its quantisation, and one expert alone in int8:
+// 24.0 / 45.5, 16.2 / 28.0, 6.3 us; 3 blocks of 256 24.4 / 46.4, 16.5 / 28.6, 6.3;
+// 10 blocks of 128 (fewer registers) 24.4 / 43.8, 15.8 / 26.9, 7.6.
+constexpr int kGvThreads = 128;
+constexpr int kGvMinBlocks = 6;
 constexpr int kGvChan = 4;                             // channels per warp
 constexpr int kGvBlockChan = kGvThreads / 32 * kGvChan;  // per block
 
