@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
 
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
-      // (grad_w: two arrivals, as a ragged stage is handed over by each CTA's clearing warp)
-      mbar_init(&full[i], kKind == kGgGradW ? 2 : 1);
+      // (grad_w in pairs: two arrivals, as a ragged stage is handed over by each CTA's clearing warp)
+      mbar_init(&full[i], kKind == kGgGradW && kPair ? 2 : 1);
       mbar_init(&empty[i], 1);
       mbar_init(&tail[i], 1);
     }
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
             mbar_arrive_expect_tx(bar, bytes);
           } else if (rank == 0) {
             mbar_arrive_expect_tx(bar, kPair ? 2 * bytes : bytes);
-            if (kKind == kGgGradW) mbar_arrive(bar);
+            if (kKind == kGgGradW && kPair) mbar_arrive(bar);
           }
           const uint32_t bar_pair = kPair ? cluster_addr(bar, rag ? rank : 0) : 0;
           auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
@@ -746,8 +746,13 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
         break;
       }
       uses ^= 1u << s;
-      clear_tail(ring + s * (uint32_t)a.stage_bytes, left, 2 + ceil_div(mma_cols(ti) >> 1, 64), lane);
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[s], 0));
+      clear_tail(ring + s * (uint32_t)a.stage_bytes, left, 2 + ceil_div(kPair ? mma_cols(ti) >> 1 : mma_cols(ti), 64), lane);
+      if (lane == 0) {
+        if (kPair)
+          mbar_arrive_cluster(cluster_addr(&full[s], 0));
+        else
+          mbar_arrive(&full[s]);
+      }
     }
   }
   __syncwarp();
@@ -828,15 +833,30 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   // 128 columns on: from 256 on costs groups of 64 rows 3% (354, 365 us), from 64
   // on int8 groups of 28 rows 6% (176, 186 us); two blocks a stage in tiles of
   // one CTA (one: e.g. 16 experts in use, 85.6 us, two 80.6, four 84.3).
+  // A product that would leave a quarter of the SMs (or pairs) without a tile
+  // takes narrower ones, its time being that of one tile: down to 128 columns,
+  // or to 64 where the depth is short and the epilogue most of a tile (int8, 905
+  // rows, [1216][384], with its quantisation: 14.3 us, 11.3 at 128, 10.1 at 64;
+  // both gradients of 2282 rows, two experts, [20128][416]: 142 us, 127 at 128,
+  // 152 at 64).  A grad_w of up to 128 channels takes tiles of one CTA, as half a
+  // pair would have nothing to do (24 rows, 40 experts, [96][7168], both
+  // gradients: 40, 31 us).
   const int64_t groups = p.rows <= 0 ? 1 : p.E < p.rows ? p.E : p.rows;
   const int64_t width = gw ? p.K : 2 * div_up(p.rows, groups);
   int cap = width <= 16 ? 16 : width <= 32 ? 32 : width <= 64 ? 64 : width <= 128 ? 128 : 256;
-  const bool pair = gw || cap >= 128;
-  if (gw && cap < 128) cap = 128;
+  if (gw && cap < 64) cap = 64;
+  bool pair = cap >= 128 && !(gw && p.N <= kChan);
+  auto col_tiles_about = [&](int c) { return gw ? p.E * div_up(p.K, c) : div_up(p.rows, c) + groups / 2; };
+  const int least = gw || a.depth * elem <= 16 * kLine ? 64 : 128;
+  while (cap > least && 4 * div_up(a.channels, pair ? 2 * kChan : kChan) * col_tiles_about(cap) <
+                            3 * (pair ? n_sms / 2 : n_sms)) {
+    cap /= 2;
+    pair = pair && cap >= 128;
+  }
   a.col_cap = cap;
   a.col_step = gw ? 64 : pair ? 32 : 16;
   const int64_t col_tiles = gw ? p.E * div_up(p.K, cap) : groups + p.rows / cap;
-  a.blocks = pair ? 1 : 2;
+  a.blocks = pair || gw ? 1 : 2;
   a.b_block = (pair ? cap / 2 : cap) * kLine;
   a.stage_bytes = a.blocks * (kABlock + a.b_block);
   a.tmem_cols = cap < 32 ? 64 : 2 * cap;  // (the epilogue reads 32 columns at a time)
@@ -889,6 +909,7 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   switch (p.kind) {
     case kGgForward: return launch_kind<kGgForward, false>(a, grid, smem, st);
     case kGgGradX: return launch_kind<kGgGradX, false>(a, grid, smem, st);
+    case kGgGradW: return launch_kind<kGgGradW, false>(a, grid, smem, st);
     default: return launch_kind<kGgInt8, false>(a, grid, smem, st);
   }
 }
