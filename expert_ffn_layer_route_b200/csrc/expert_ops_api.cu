@@ -72,8 +72,7 @@ GroupedProblem problem(int kind, const moe_gemm_desc& d, const Pitch& t) {
 moe_status check_rows(int rows, int width, int dtype) {
   if (rows < 0 || width <= 0 || !is16(dtype)) return MOE_ERR_INVALID_ARG;
   if (width > kMaxExtent || rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
-  // one block per 256 values at the least
-  if ((int64_t)rows * ((width + 255) / 256) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)rows * width > (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

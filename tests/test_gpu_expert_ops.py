@@ -591,10 +591,61 @@ def test_quant_rows_bit_for_bit(R, K, extra, t):
     assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
 
 
-def test_quant_rows_gather_and_odd_rows():
+LENGTHS = [1, 2, 30, 78, 250, 256, 257, 510, 1000, 1023, 1026, 2050, 4098, 5001, 8194, 15360, 15362]
+
+
+def laid_out(shape, dtype, how):
+    """A buffer whose rows start on 16-byte boundaries, side by side, or 2 values apart on an odd address."""
+    if how == "pitched":
+        return pitched(shape, dtype)
+    gap = {"side_by_side": 0, "apart": 2}[how]
+    flat = torch.zeros(shape[0] * (shape[1] + gap) + 1, dtype=dtype, device=DEV)
+    return (flat[:-1] if gap == 0 else flat[1:]).view(shape[0], shape[1] + gap)[:, : shape[1]]
+
+
+@pytest.mark.parametrize("K", LENGTHS)
+@pytest.mark.parametrize("hx,hq", [("pitched", "pitched"), ("side_by_side", "side_by_side"), ("apart", "pitched"),
+                                   ("pitched", "apart")])
+def test_row_operators_over_lengths_and_layouts(K, hx, hq):
+    g = gen(27)
+    R = 11
+    x = laid_out((R, K), BF16, hx).copy_(torch.randn(R, K, generator=g, device=DEV))
+    q, s = laid_out((R, K), torch.int8, hq), torch.empty(R, device=DEV)
+    base = q._base if q._base is not None else q
+    base.fill_(99)
+    moe.moe_quant_rows_i8(x, q, s)
+    ok()
+    rq, rs = ref_codes(x.float().cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
+    assert int((base != 99).sum()) <= R * K  # nothing between the rows
+    gu = laid_out((R, 2 * K), BF16, hx).copy_(torch.randn(R, 2 * K, generator=g, device=DEV) * 2)
+    dh = laid_out((R, K), BF16, hq).copy_(torch.randn(R, K, generator=g, device=DEV))
+    h, d = laid_out((R, K), BF16, hq), laid_out((R, 2 * K), BF16, hq)
+    moe.moe_swiglu(gu, h)
+    moe.moe_swiglu_grad(gu, dh, d)
+    moe.moe_swiglu_quant_i8(gu, q, s)
+    ok()
+    a = gu.double().requires_grad_()
+    ga, ua = a[:, :K], a[:, K:]
+    ref = ga * torch.sigmoid(ga) * ua
+    ref.backward(dh.double())
+    ga, v = ga.detach(), ref.detach()
+    n = swiglu_ulps(ga)
+    check(h, v, v.abs() * n * U)
+    sg = torch.sigmoid(ga)
+    m = (dh.double() * ua.detach() * sg).abs() * (1 + ga.abs() * (1 - sg + n * U))
+    check(d[:, :K], a.grad[:, :K], m * 2 * n * U)
+    check(d[:, K:], a.grad[:, K:], a.grad[:, K:].abs() * n * U)
+    rel, amax = n.max() * U, v.abs().amax(1)
+    assert bool(((s.double() - amax / 127).abs() <= amax / 127 * (rel + U)).all())
+    assert bool(((v / (amax / 127)[:, None] - q.double()).abs() <= 0.5 + 127 * (2 * rel + 2 * U)).all())
+
+
+@pytest.mark.parametrize("K", [264, 1500])
+def test_quant_rows_gather_and_odd_rows(K):
     """Rows by token, one token for several rows, dropped pairs; NaN, infinities, the smallest and largest values."""
     g = gen(12)
-    x = normal((6, 264), BF16, g)
+    x = normal((6, K), BF16, g)
     x[1, 7] = float("nan")
     x[2, 9] = -float("inf")
     x[3] = torch.finfo(BF16).max
@@ -602,7 +653,7 @@ def test_quant_rows_gather_and_odd_rows():
     x[5] = 0
     x[5, 263] = -(2.0 ** -120)
     tok = torch.tensor([5, 0, 0, 2, 3, -1, 6, 4, 1, 0, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
-    q = torch.full((11, 264), 99, dtype=torch.int8, device=DEV)
+    q = torch.full((11, K), 99, dtype=torch.int8, device=DEV)
     s = torch.full((11,), 99.0, device=DEV)
     moe.moe_quant_rows_i8(x, q, s, row_token=tok)
     ok()
