@@ -45,8 +45,8 @@ moe_status check_gemm(const moe_gemm_desc* d, bool int8, Pitch* t) {
 moe_status run(const GroupedProblem& p, void* stream) {
   const DevInfo di = dev_info();
   int unsupported = 0;
-  if (grouped_gemv_pays(p)) {
-    const cudaError_t err = launch_grouped_gemv(p, static_cast<cudaStream_t>(stream));
+  if (grouped_gemv_pays(p, di.sms)) {
+    const cudaError_t err = launch_grouped_gemv(p, di.sms, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   const cudaError_t err = launch_grouped_gemm(p, di.sms, di.smem_optin, static_cast<cudaStream_t>(stream),

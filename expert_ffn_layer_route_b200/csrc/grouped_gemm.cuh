@@ -43,7 +43,7 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
 
 // The same products (forward, int8) for few rows: csrc/grouped_gemv.cu, and
 // whether that kernel is the faster one.
-bool grouped_gemv_pays(const GroupedProblem& p);
-cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st);
+bool grouped_gemv_pays(const GroupedProblem& p, int n_sms);
+cudaError_t launch_grouped_gemv(const GroupedProblem& p, int n_sms, cudaStream_t st);
 
 }  // namespace moe

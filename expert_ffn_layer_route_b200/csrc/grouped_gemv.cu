@@ -26,7 +26,7 @@ namespace {
 constexpr int kGvThreads = 128;
 constexpr int kGvMinBlocks = 6;
 constexpr int kGvChan = 4;                             // channels per warp
-constexpr int kGvBlockChan = kGvThreads / 32 * kGvChan;  // per block
+constexpr int kGvWarps = kGvThreads / 32;
 
 struct GemvArgs {
   const uint8_t* w;
@@ -120,9 +120,12 @@ __device__ __forceinline__ void dot(const uint4 (&w)[kGvChan], const uint4 (&x)[
   }
 }
 
-// R rows from `row` on, the warp's channels from ch0 on.
-template <int kType, int R>
-__device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0, int phys, int lane) {
+// R rows from `row` on, the warp's channels from ch0 on.  kSplit: the block's
+// warps share the channels, each takes every kGvWarps-th piece of the depth, and
+// the first one adds their sums in order.
+template <int kType, int R, bool kSplit>
+__device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0, int phys, int warp, int lane) {
+  constexpr int kStep = kSplit ? 512 * kGvWarps : 512;
   using S = typename Sum<kType>::T;
   const uint8_t* w[kGvChan];
   const uint8_t* x[R];
@@ -137,22 +140,22 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[c][r] = 0;
   const int whole = a.depth_bytes & ~15;
-  int b = lane * 16;
-  for (; b + 512 < whole; b += 1024) {
+  int b = lane * 16 + (kSplit ? warp * 512 : 0);
+  for (; b + kStep < whole; b += 2 * kStep) {
     uint4 w0[kGvChan], w1[kGvChan], x0[R], x1[R];
 #pragma unroll
     for (int c = 0; c < kGvChan; ++c) w0[c] = load_stream(w[c] + b);
 #pragma unroll
-    for (int c = 0; c < kGvChan; ++c) w1[c] = load_stream(w[c] + b + 512);
+    for (int c = 0; c < kGvChan; ++c) w1[c] = load_stream(w[c] + b + kStep);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       x0[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b));
-      x1[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b + 512));
+      x1[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b + kStep));
     }
     dot<kType, R>(w0, x0, acc);
     dot<kType, R>(w1, x1, acc);
   }
-  for (; b < a.depth_bytes; b += 512) {
+  for (; b < a.depth_bytes; b += kStep) {
     const int n = a.depth_bytes - b;
     uint4 w0[kGvChan], x0[R];
 #pragma unroll
@@ -173,14 +176,25 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[c][r] += __shfl_xor_sync(0xffffffffu, acc[c][r], o);
+  S s = 0;
+#pragma unroll
+  for (int c = 0; c < kGvChan; ++c)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r * kGvChan + c == lane) s = acc[c][r];
+  if constexpr (kSplit) {
+    __shared__ S part[kGvWarps][kGvChan * R];
+    if (lane < kGvChan * R) part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && lane < kGvChan * R) {
+#pragma unroll
+      for (int o = 1; o < kGvWarps; ++o) s += part[o][lane];
+    }
+    __syncthreads();  // (the next rows' sums come to the same place)
+    if (warp != 0) return;
+  }
   if (lane < kGvChan * R) {
     const int lr = lane / kGvChan, ch = ch0 + lane % kGvChan;
-    S s = 0;
-#pragma unroll
-    for (int c = 0; c < kGvChan; ++c)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (r * kGvChan + c == lane) s = acc[c][r];
     if (ch < a.channels) {
       float f = (float)s;
       if constexpr (kType == kI8)
@@ -201,7 +215,7 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
 // Grid: (channel blocks, rows); the blocks of a group's first row serve the
 // whole group, those of its other rows end at once, so that a group's weights
 // are read once whatever the routing.
-template <int kType>
+template <int kType, bool kSplit>
 __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(const GemvArgs a) {
   __shared__ int s_n, s_phys;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -227,13 +241,30 @@ __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(
     }
   }
   __syncthreads();
-  const int n = s_n, phys = s_phys;
-  const int ch0 = blockIdx.x * kGvBlockChan + (tid >> 5) * kGvChan;
+  const int n = s_n, phys = s_phys, warp = tid >> 5;
+  const int ch0 = (kSplit ? blockIdx.x : blockIdx.x * kGvWarps + warp) * kGvChan;
   if (n == 0 || ch0 >= a.channels) return;
   int r = 0;
-  for (; r + 2 <= n; r += 2) rows_of<kType, 2>(a, row + r, ch0, phys, lane);
-  if (r < n) rows_of<kType, 1>(a, row + r, ch0, phys, lane);
+  for (; r + 2 <= n; r += 2) rows_of<kType, 2, kSplit>(a, row + r, ch0, phys, warp, lane);
+  if (r < n) rows_of<kType, 1, kSplit>(a, row + r, ch0, phys, warp, lane);
 }
+
+namespace {
+
+int64_t groups_of(const GroupedProblem& p) { return p.E < p.rows ? p.E : p.rows; }
+int depth_bytes_of(const GroupedProblem& p) { return p.K * (p.kind == kGgInt8 ? 1 : 2); }
+int64_t blocks_of(const GroupedProblem& p) { return ((int64_t)p.N + kGvWarps * kGvChan - 1) / (kGvWarps * kGvChan); }
+
+// Few channels: a block to 4 of them, its warps along the depth, where whole
+// warps would leave SMs idle (one expert, bf16, one row: [1275][10200] 17.2 us,
+// split 7.6; [2080][3488] 5.5, 4.9; [5760][2880] 9.6, 8.9, but with half the
+// depth's bytes, in int8, 8.2, 9.7).
+bool split_depth(const GroupedProblem& p, int n_sms) {
+  const int64_t blocks = groups_of(p) * blocks_of(p);
+  return blocks < n_sms || (blocks < 3 * n_sms && depth_bytes_of(p) >= 4096);
+}
+
+}  // namespace
 
 // Up to 12 rows (int8: 16) and about two per expert in use; measured against the
 // tensor-core kernel (us, this kernel first): gpt-oss-shaped bf16 gate/up, 128
@@ -242,12 +273,16 @@ __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(
 // 24.6 / 39.0 / 43.8 / 50.0; one such expert, 1 / 2 / 4 rows 9.6 / 12.4 / 17.8
 // against 14.2 / 13.9 / 14.1; the tiny layer's 16 / 32 rows 5.0 / 6.7 against
 // 4.9 / 4.9.
-bool grouped_gemv_pays(const GroupedProblem& p) {
+// With few channels 128-channel tiles leave most SMs idle: then up to six rows
+// per expert ([1275][10200] with 5 / 12 rows 16.0 / 32.2 against 36.3 / 36.9,
+// [2080][3488] with 5 / 8 rows 11.6 / 15.1 against 13.0).
+bool grouped_gemv_pays(const GroupedProblem& p, int n_sms) {
   if (p.kind != kGgForward && p.kind != kGgInt8) return false;
-  return p.rows <= (p.kind == kGgInt8 ? 16 : 12) && p.rows <= 2 * (p.E < p.rows ? p.E : p.rows);
+  const int64_t per_expert = split_depth(p, n_sms) ? 6 : 2;
+  return p.rows <= (p.kind == kGgInt8 ? 16 : 12) && p.rows <= per_expert * groups_of(p);
 }
 
-cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st) {
+cudaError_t launch_grouped_gemv(const GroupedProblem& p, int n_sms, cudaStream_t st) {
   GemvArgs a;
   a.w = static_cast<const uint8_t*>(p.a);
   a.x = static_cast<const uint8_t*>(p.b);
@@ -264,13 +299,15 @@ cudaError_t launch_grouped_gemv(const GroupedProblem& p, cudaStream_t st) {
   a.rows = p.rows;
   a.n_phys = p.n_phys;
   a.channels = p.N;
-  a.depth_bytes = p.K * (p.kind == kGgInt8 ? 1 : 2);
+  a.depth_bytes = depth_bytes_of(p);
   a.out_dtype = p.out_dtype;
   ProfScope prof(p.kind == kGgInt8 ? "grouped_gemm_i8" : "grouped_gemm", st);
-  const dim3 grid((p.N + kGvBlockChan - 1) / kGvBlockChan, p.rows);
-  auto k = p.kind == kGgInt8           ? grouped_gemv_kernel<kI8>
-           : p.dtype == MOE_T_BF16 ? grouped_gemv_kernel<kBf16>
-                                       : grouped_gemv_kernel<kFp16>;
+  const bool split = split_depth(p, n_sms);
+  const dim3 grid((unsigned)(split ? (p.N + kGvChan - 1) / kGvChan : blocks_of(p)), p.rows);
+  auto k = p.kind == kGgInt8 ? (split ? grouped_gemv_kernel<kI8, true> : grouped_gemv_kernel<kI8, false>)
+           : p.dtype == MOE_T_BF16
+               ? (split ? grouped_gemv_kernel<kBf16, true> : grouped_gemv_kernel<kBf16, false>)
+               : (split ? grouped_gemv_kernel<kFp16, true> : grouped_gemv_kernel<kFp16, false>);
   return launch_pdl(k, grid, dim3(kGvThreads), 0, st, a);
 }
 

@@ -425,7 +425,8 @@ def test_results_past_32_bit_offsets():
 # rows of each expert, N, K: a handful of rows, where a kernel of its own runs, and just past it
 FEW = [([1] * 4, 130, 264), ([0, 1, 0, 2, 0, 0, 1], 33, 17), ([2, 0, 1], 257, 1), ([1] * 12, 64, 2880),
        ([1] * 13, 64, 2880), ([1] * 16, 40, 5000), ([1] * 17, 40, 5000), ([5, 1, 1, 1, 0, 0, 0, 0], 96, 520),
-       ([2], 100, 300), ([3], 100, 300), ([0] * 1023 + [1], 35, 1031)]
+       ([2], 100, 300), ([3], 100, 300), ([0] * 1023 + [1], 35, 1031), ([6], 70, 4099), ([7], 70, 4099),
+       ([1, 5, 4], 129, 2600), ([2, 3], 5, 9), ([4], 2, 130), ([6, 6], 300, 8200)]
 
 
 @pytest.mark.parametrize("counts,N,K", FEW, ids=[f"{sum(c)}of{len(c)}" for c, _, _ in FEW])
