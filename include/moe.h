@@ -8,6 +8,9 @@
  *   weighted combine back to token order (+ shared experts),
  *
  * plus an HBM expert cache filled from a pinned host-memory expert bank.
+ * The expert FFN's parts are also calls of their own ("Expert operators" below):
+ * grouped products with their gradients, the same product in 8-bit integers,
+ * SwiGLU with its gradient.
  *
  * What the pages define, and where:
  *  - "Each MoE layer replaces the dense feed-forward block with many smaller
@@ -247,7 +250,8 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, const vo
  * of whole 16 bytes.  Outputs need only the alignment of their type; pitches
  * of whole 16 bytes are stored faster.
  * No call needs a workspace; none allocates.  All may be captured into a
- * CUDA graph.  Outputs must not overlap inputs unless a call says so.
+ * CUDA graph.  While they run, the blocks of the grouped products hold an SM's
+ * shared memory and up to 512 columns of its tensor memory.  Outputs must not overlap inputs unless a call says so.
  * ---------------------------------------------------------------------- */
 typedef enum { MOE_T_BF16 = 0, MOE_T_FP16 = 1, MOE_T_FP32 = 2, MOE_T_INT8 = 3 } moe_dtype;
 
