@@ -182,7 +182,8 @@ __device__ __forceinline__ void row_values(const T* p, int c, int K, float (&v)[
       float u[W];
       load<T, W>(p + K + c, u);
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
+      for (int i = 0; i < W; ++i)  // exactly rounded steps: approximate ones turn codes over that lie next to a border
+        v[i] = __fmul_rn(__fdiv_rn(v[i], __fadd_rn(1.f, expf(-v[i]))), u[i]);
     }
   } else {
 #pragma unroll
@@ -257,8 +258,9 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 // L1/L2.  A row's loads, its maximum and its stores come one after the other, so
 // what fills an SM is rows side by side: small blocks, 8 of 128 threads (3 of 384
 // for long rows).  Measured: 8192 rows of 4096, 34 us against 45 with 2 blocks of
-// 512; SwiGLU of 8192 x 14336 into codes 134 us (4.4 TB/s) against 154.  A
-// persistent block that copies rows ahead into shared memory took 60 and 140 us.
+// 512; SwiGLU of 8192 x 14336 into codes 134 us (4.4 TB/s) against 154 (180 with
+// the exactly rounded steps that it takes now).  A persistent block that copies
+// rows ahead into shared memory took 60 and 140 us.
 template <typename T, bool kSwiglu, int W, int V, int NT>
 __global__ void __launch_bounds__(NT, NT == 384 ? 3 : 1024 / NT)
     quant_rows_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ row_token, int n_tokens,

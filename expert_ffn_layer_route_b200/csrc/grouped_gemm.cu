@@ -41,6 +41,12 @@ constexpr int kChan = 128;             // channels per CTA and tile: the TMEM la
 constexpr int kLine = 128;             // bytes of the contraction per K-major block (one swizzle line)
 constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction rows x 64 channels of 16 bits
 constexpr int kABlock = kChan * kLine;  // the channels' operand of a block, either way
+// The tensor cores cut their fp32 additions short (they do not round them): over
+// 3500 products a sum comes out 4e-6 off, over 9000 1.1e-5.  A 16-bit result does
+// not show it.  An fp32 one is summed in pieces, each by its own accumulator, which
+// the epilogue adds in fp32 (under 1e-6 whatever the depth; the result's lines
+// are read and written again for each, mostly in L2).  int8 sums are exact.
+constexpr int kPiece = 640;  // contraction elements (a multiple of a step's, 64 or 128)
 constexpr int kMaxStages = 12;
 constexpr int64_t kMaxTiles = (int64_t)1 << 30;
 // A warp reads the 32 TMEM lanes of its quadrant.  grad_w has two warps to a
@@ -218,9 +224,13 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
   const int r0 = lane / kPieces, b = lane % kPieces * kBytes;
   const uint32_t s = staged + r0 * kPitch + (kSwizzled ? (((b >> 4) ^ r0) << 4 | (b & 15)) : b);
   uint8_t* d = out + r0 * pitch + b;
-  auto put = [&](uint8_t* p, const uint32_t(&t)[kWords], float old) {
-    if constexpr (kAdd)
-      *reinterpret_cast<float*>(p) = old + __uint_as_float(t[0]);
+  static_assert(!kAdd || kWords != 2, "sums are added 4 or 16 bytes at a time");
+  auto put = [&](uint8_t* p, const uint32_t(&t)[kWords], const float(&old)[kWords]) {
+    if constexpr (kAdd && kWords == 4)
+      *reinterpret_cast<float4*>(p) = make_float4(old[0] + __uint_as_float(t[0]), old[1] + __uint_as_float(t[1]),
+                                                  old[2] + __uint_as_float(t[2]), old[3] + __uint_as_float(t[3]));
+    else if constexpr (kAdd)
+      *reinterpret_cast<float*>(p) = old[0] + __uint_as_float(t[0]);
     else if constexpr (kWords == 4)
       st_global16(p, make_uint4(t[0], t[1], t[2], t[3]));
     else if constexpr (kWords == 2)
@@ -236,7 +246,7 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
 #pragma unroll 1
     for (int i0 = 0; i0 * kRows < n; i0 += kBatch) {
       uint32_t t[kBatch][kWords];
-      float old[kBatch];
+      float old[kBatch][kWords];
       uint8_t* p[kBatch];
       const int left = n - r0 - i0 * kRows;  // rows from this lane's first on
 #pragma unroll
@@ -244,7 +254,17 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
         lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + (i0 + i) * kRows * kPitch, t[i]);
         p[i] = d;
         d += kRows * pitch;
-        if (kAdd && i * kRows < left) old[i] = *reinterpret_cast<const float*>(p[i]);
+        if (kAdd && i * kRows < left) {
+          if constexpr (kWords == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(p[i]);
+            old[i][0] = f.x;
+            old[i][1] = f.y;
+            old[i][2] = f.z;
+            old[i][3] = f.w;
+          } else if constexpr (kWords == 1) {
+            old[i][0] = *reinterpret_cast<const float*>(p[i]);
+          }
+        }
       }
       if (left >= (kBatch - 1) * kRows + 1) {
 #pragma unroll
@@ -260,19 +280,30 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
     for (int r = r0, i = 0; r < n; r += kRows, ++i, d += kRows * pitch) {
       uint32_t t[kWords];
       lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + i * kRows * kPitch, t);
+      if constexpr (kAdd) {
 #pragma unroll
-      for (int z = 0; z < kBytes; z += 2)
-        if (b + z < width) *reinterpret_cast<uint16_t*>(d + z) = (uint16_t)(t[z >> 2] >> (8 * (z & 2)));
+        for (int z = 0; z < kWords; ++z)
+          if (b + 4 * z < width) *reinterpret_cast<float*>(d + 4 * z) += __uint_as_float(t[z]);
+      } else {
+#pragma unroll
+        for (int z = 0; z < kBytes; z += 2)
+          if (b + z < width) *reinterpret_cast<uint16_t*>(d + z) = (uint16_t)(t[z >> 2] >> (8 * (z & 2)));
+      }
     }
   }
 }
 
 // rows of 32 channels, kElem bytes each (out of line: the common case stays small)
-template <int kElem>
+template <int kElem, bool kInPieces>
 __device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
-                                            int lane) {
+                                            int add, int lane) {
   constexpr int kRow = 32 * kElem, kStaged = kElem == 4 ? kPitch32 : kPitch16;
-  if (vec == 16)
+  if (kInPieces && add) {
+    if (vec == 16)
+      store_pieces<16, kRow, kStaged, false, true>(out, pitch, staged, n, width, lane);
+    else
+      store_pieces<4, kRow, kStaged, false, true>(out, pitch, staged, n, width, lane);
+  } else if (vec == 16)
     store_pieces<16, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
   else if (vec == 8)
     store_pieces<8, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
@@ -284,9 +315,12 @@ __device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, uint32_
 
 // lines of 128 bytes, their 16-byte pieces swizzled (in line: a call here would have to save the columns that
 // are on their way from tensor memory)
+template <bool kInPieces>
 __device__ __forceinline__ void store_lines_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
                                              int add, int lane) {
-  if (add)
+  if (kInPieces && add && vec == 16)
+    store_pieces<16, 128, 128, true, true>(out, pitch, staged, n, width, lane);
+  else if (kInPieces && add)
     store_pieces<4, 128, 128, true, true>(out, pitch, staged, n, width, lane);
   else if (vec == 16)
     store_pieces<16, 128, 128, true, false>(out, pitch, staged, n, width, lane);
@@ -304,7 +338,8 @@ __device__ __forceinline__ void store_lines_any(uint8_t* out, int64_t pitch, uin
 // channels: each loads its 128 channels of A and half of the columns of B, the
 // even CTA issues one MMA for both, and each keeps its 128 channels of D.  Each
 // operand byte then crosses L2 -> SM half as often as with tiles of one CTA.
-template <int kKind, bool kPair>
+// kF32: the result is fp32, and a sum is taken kPiece products at a time.
+template <int kKind, bool kPair, bool kF32>
 __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(const __grid_constant__ GgArgs a) {
   constexpr bool kAChanMajor = kKind == kGgGradX || kKind == kGgGradW;  // A rows run along the channels
   constexpr bool kBChanMajor = kKind == kGgGradW;
@@ -314,6 +349,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
   constexpr int kColRound = kPair ? 32 : 16;
   constexpr int kEpiBytes = epi_bytes(kKind), kEpiWarps = epi_warps(kKind);
   constexpr int kTileChan = kPair ? 2 * kChan : kChan;
+  constexpr bool kInPieces = kF32 && kKind != kGgInt8;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = uni(tid >> 5);
@@ -543,16 +579,20 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       const Tile ti = tile_at(t);
       const int depth = uni(depth_of(ti));
       const int ncols = uni(mma_cols(ti));
-      const int buf = i & 1;
-      if (warp_any(*s_abort) || !warp_wait<kPair>(&acc_empty[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
-        *s_abort = 1;
-        break;
-      }
-      tc::fence_after_sync();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(buf * a.col_cap);
       const uint32_t idesc = a.idesc | ((uint32_t)(ncols >> 3) << 17);
-      for (int d0 = 0; d0 < depth; d0 += step_depth) {
+      uint32_t d_tmem = 0;
+      int d0 = 0, in_piece = 0;  // (in_piece: what the accumulator holds already)
+      do {
+        if ((kInPieces ? in_piece : d0) == 0) {  // the next accumulator
+          if (warp_any(*s_abort) || !warp_wait<kPair>(&acc_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+            *s_abort = 1;
+            break;
+          }
+          tc::fence_after_sync();
+          d_tmem = tmem_base + (uint32_t)((i & 1) * a.col_cap);
+        }
         const int left = depth - d0;
+        if (left <= 0) break;  // an empty group
         if (!warp_wait<kPair>(&full[s], par)) {
           *s_abort = 1;
           break;
@@ -565,7 +605,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
         constexpr int kStepA = kAChanMajor ? 128 : 2, kStepB = kBChanMajor ? 128 : 2;
         uint64_t da = a_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
         uint64_t db = b_desc0 + (uint64_t)(s * (uint32_t)(a.stage_bytes >> 4));
-        uint32_t more = d0 != 0;
+        uint32_t more = (kInPieces ? in_piece : d0) != 0;
         for (int l = left; l > 0 && l > left - step_depth; l -= kDepthBlock) {
           if (l >= kDepthBlock) {
             if (tc::elect_one()) {
@@ -589,9 +629,18 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
           s = 0;
           par ^= 1;
         }
-      }
+        d0 += step_depth;
+        if constexpr (kInPieces) {
+          in_piece += step_depth;
+          if (in_piece >= kPiece && d0 < depth) {  // a piece of the sum is complete
+            if (tc::elect_one()) tc::commit_g<kPair>(&acc_full[i & 1]);
+            ++i;
+            in_piece = 0;
+          }
+        }
+      } while (d0 < depth);
       if (warp_any(*s_abort)) break;
-      if (tc::elect_one()) tc::commit_g<kPair>(&acc_full[buf]);  // (an empty group: at once)
+      if (tc::elect_one()) tc::commit_g<kPair>(&acc_full[i & 1]);  // (an empty group: at once)
       __syncwarp();
     }
     if (rank == 0) {  // every MMA has completed before TMEM is freed
@@ -603,133 +652,137 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
     // ================================================================ epilogue
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     uint8_t* stage_o = epi + (warp - 2) * kEpiBytes;
-    const int osz = a.out_dtype == MOE_T_FP32 ? 4 : 2;
+    constexpr int osz = kF32 ? 4 : 2;
     int i = 0;
-    for (int t = unit; t < total_tiles; t += units, ++i) {
+    for (int t = unit; t < total_tiles; t += units) {
       const Tile ti = tile_at(t);
-      const int buf = i & 1;
-      if (warp_any(*s_abort) || !warp_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
-        *s_abort = 1;
-        break;
-      }
-      tc::fence_after_sync();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.col_cap);
-      const int ch0 = ti.m0 + rank * kChan + q * 32;
-      const bool mine = ch0 < a.channels;
-      if (!mine) {
-      } else if constexpr (kKind == kGgGradW) {
-        // 32 rows n of dw, 128 bytes of k at a time: a thread holds one row's
-        // line; through shared memory the lines leave 8 lanes to a line
-        const int per_line = 128 / osz;
-        uint8_t* const o = static_cast<uint8_t*>(a.out) +
-                           ((int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0) * osz;
-        const int64_t op = a.ldo * osz;
-        const int n = min(32, a.channels - ch0);
-        const int first = (warp - 2) / 4 * per_line, step = 2 * per_line;
-        uint32_t v[32];
-        if (first < ti.nc) tc::ld_issue32(taddr + first, v);
-        for (int j0 = first; j0 < ti.nc; j0 += step) {
-          tc::ld_wait32(v);
-          uint4* line = reinterpret_cast<uint4*>(stage_o + lane * 128);
-          if (ti.n == 0) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) line[c ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
-          } else if (osz == 4) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              line[c ^ (lane & 7)] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          } else {
-            auto half_line = [&](int c0) {
-              auto two = [&](int j) {
-                return pack16(a.out_dtype, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-              };
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                line[(c0 + c) ^ (lane & 7)] = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
-            };
-            half_line(0);
-            tc::ld_issue32(taddr + j0 + 32, v);
-            tc::ld_wait32(v);
-            half_line(4);
-          }
-          __syncwarp();
-          const int width = min(128, (ti.nc - j0) * osz);
-          const bool wide = a.vec == 16 && width == 128 && !a.accumulate;
-          // the next line's values come while this one's leave (not across a call: they arrive in registers)
-          auto issue_next = [&] {
-            if (j0 + step < ti.nc) tc::ld_issue32(taddr + j0 + step, v);
-          };
-          if (wide) {
-            issue_next();
-            const uint32_t base = smem_u32(stage_o);
-            store_lines<8>(o + j0 * osz, op, n, lane,
-                           [&](int r, int p) { return base + r * 128 + ((p ^ (r & 7)) << 4); });
-          } else {
-            store_lines_any(o + j0 * osz, op, smem_u32(stage_o), n, width, a.vec, a.accumulate, lane);
-            __syncwarp();
-            issue_next();
-          }
-          __syncwarp();
+      // (the pieces of a tile's sum come one after the other: the first is stored, the others are added)
+      for (int d0 = 0, more = 1; more; ++i) {
+        const int buf = i & 1;
+        if (warp_any(*s_abort) || !warp_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
+          *s_abort = 1;
+          break;
         }
-      } else {
-        // 32 rows x 32 channels at a time: a thread holds one channel of 32
-        // rows; through shared memory a row's channels leave side by side
-        float sw = 0.f;
-        if (kKind == kGgInt8 && ch0 + lane < a.channels)
-          sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
-        const int64_t row0 = (int64_t)ti.row0 + ti.c0;
-        const int width = min(32, a.channels - ch0) * osz;
-        uint32_t v[32];
-        tc::ld_issue32(taddr, v);
-        for (int j0 = 0; j0 < ti.nc; j0 += 32) {
-          float sx = 0.f;
-          if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
-          tc::ld_wait32(v);
-          const int n = min(32, ti.nc - j0);
-#pragma unroll
-          for (int g = 0; g < 32; g += 8) {
-            if (g >= n) break;
-#pragma unroll
-            for (int j = g; j < g + 8; ++j) {
-              float f = __uint_as_float(v[j]);
-              if constexpr (kKind == kGgInt8) f = (float)(int)v[j] * (__shfl_sync(0xffffffffu, sx, j) * sw);
-              if (osz == 4)
-                *reinterpret_cast<float*>(stage_o + j * kPitch32 + lane * 4) = f;
-              else
-                *reinterpret_cast<uint16_t*>(stage_o + j * kPitch16 + lane * 2) = (uint16_t)pack16(a.out_dtype, f, 0.f);
-            }
-          }
-          __syncwarp();
-          // the next rows' values come while these leave (not across a call: they arrive in registers)
-          const bool next = j0 + 32 < ti.nc;
-          const bool wide = a.vec == 16 && width == 32 * osz;
-          if (next && wide) tc::ld_issue32(taddr + j0 + 32, v);
-          uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
+        const int add = kInPieces && (d0 > 0 || a.accumulate);
+        d0 += kPiece;
+        more = kInPieces && d0 < depth_of(ti);
+        tc::fence_after_sync();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.col_cap);
+        const int ch0 = ti.m0 + rank * kChan + q * 32;
+        const bool mine = ch0 < a.channels;
+        if (!mine) {
+        } else if constexpr (kKind == kGgGradW) {
+          // 32 rows n of dw, 128 bytes of k at a time: a thread holds one row's
+          // line; through shared memory the lines leave 8 lanes to a line
+          const int per_line = 128 / osz;
+          uint8_t* const o = static_cast<uint8_t*>(a.out) +
+                             ((int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0) * osz;
           const int64_t op = a.ldo * osz;
-          const uint32_t base = smem_u32(stage_o);
-          if (!wide) {
-            if (osz == 4)
-              store_rows_any<4>(o, op, base, n, width, a.vec, lane);
-            else
-              store_rows_any<2>(o, op, base, n, width, a.vec, lane);
+          const int n = min(32, a.channels - ch0);
+          const int first = (warp - 2) / 4 * per_line, step = 2 * per_line;
+          uint32_t v[32];
+          if (first < ti.nc) tc::ld_issue32(taddr + first, v);
+          for (int j0 = first; j0 < ti.nc; j0 += step) {
+            tc::ld_wait32(v);
+            uint4* line = reinterpret_cast<uint4*>(stage_o + lane * 128);
+            if (ti.n == 0) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) line[c ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
+            } else if (osz == 4) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                line[c ^ (lane & 7)] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            } else {
+              auto half_line = [&](int c0) {
+                auto two = [&](int j) {
+                  return pack16(a.out_dtype, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                };
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  line[(c0 + c) ^ (lane & 7)] = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+              };
+              half_line(0);
+              tc::ld_issue32(taddr + j0 + 32, v);
+              tc::ld_wait32(v);
+              half_line(4);
+            }
             __syncwarp();
-            if (next) tc::ld_issue32(taddr + j0 + 32, v);
-          } else if (osz == 4) {
-            store_lines<8>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch32 + p * 16; });
-          } else {
-            store_lines<4>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch16 + p * 16; });
+            const int width = min(128, (ti.nc - j0) * osz);
+            const bool wide = a.vec == 16 && width == 128 && !add;
+            // the next line's values come while this one's leave (not across a call: they arrive in registers)
+            auto issue_next = [&] {
+              if (j0 + step < ti.nc) tc::ld_issue32(taddr + j0 + step, v);
+            };
+            if (wide) {
+              issue_next();
+              const uint32_t base = smem_u32(stage_o);
+              store_lines<8>(o + j0 * osz, op, n, lane,
+                             [&](int r, int p) { return base + r * 128 + ((p ^ (r & 7)) << 4); });
+            } else {
+              store_lines_any<kInPieces>(o + j0 * osz, op, smem_u32(stage_o), n, width, a.vec, add, lane);
+              __syncwarp();
+              issue_next();
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        } else {
+          // 32 rows x 32 channels at a time: a thread holds one channel of 32
+          // rows; through shared memory a row's channels leave side by side
+          float sw = 0.f;
+          if (kKind == kGgInt8 && ch0 + lane < a.channels)
+            sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
+          const int64_t row0 = (int64_t)ti.row0 + ti.c0;
+          const int width = min(32, a.channels - ch0) * osz;
+          uint32_t v[32];
+          tc::ld_issue32(taddr, v);
+          for (int j0 = 0; j0 < ti.nc; j0 += 32) {
+            float sx = 0.f;
+            if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
+            tc::ld_wait32(v);
+            const int n = min(32, ti.nc - j0);
+#pragma unroll
+            for (int g = 0; g < 32; g += 8) {
+              if (g >= n) break;
+#pragma unroll
+              for (int j = g; j < g + 8; ++j) {
+                float f = __uint_as_float(v[j]);
+                if constexpr (kKind == kGgInt8) f = (float)(int)v[j] * (__shfl_sync(0xffffffffu, sx, j) * sw);
+                if (osz == 4)
+                  *reinterpret_cast<float*>(stage_o + j * kPitch32 + lane * 4) = f;
+                else
+                  *reinterpret_cast<uint16_t*>(stage_o + j * kPitch16 + lane * 2) = (uint16_t)pack16(a.out_dtype, f, 0.f);
+              }
+            }
+            __syncwarp();
+            // the next rows' values come while these leave (not across a call: they arrive in registers)
+            const bool next = j0 + 32 < ti.nc;
+            const bool wide = a.vec == 16 && width == 32 * osz && !add;
+            if (next && wide) tc::ld_issue32(taddr + j0 + 32, v);
+            uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
+            const int64_t op = a.ldo * osz;
+            const uint32_t base = smem_u32(stage_o);
+            if (!wide) {
+              store_rows_any<osz, kInPieces>(o, op, base, n, width, a.vec, add, lane);
+              __syncwarp();
+              if (next) tc::ld_issue32(taddr + j0 + 32, v);
+            } else if (osz == 4) {
+              store_lines<8>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch32 + p * 16; });
+            } else {
+              store_lines<4>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch16 + p * 16; });
+            }
+            __syncwarp();
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair)
+            mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
+          else
+            mbar_arrive(&acc_empty[buf]);
         }
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if (kPair)
-          mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
-        else
-          mbar_arrive(&acc_empty[buf]);
-      }
+      if (warp_any(*s_abort)) break;
     }
   }
   if (kKind == kGgGradW && warp == 2 + kEpiWarps) {
@@ -767,9 +820,9 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
 // ------------------------------------------------------------------ host side
 namespace {
 
-template <int kKind, bool kPair>
-cudaError_t launch_kind(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
-  cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind, kPair>>(smem);
+template <int kKind, bool kPair, bool kF32>
+cudaError_t launch_as(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
+  cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind, kPair, kF32>>(smem);
   if (err != cudaSuccess) return err;
   static const char* const names[4] = {"grouped_gemm", "grouped_gemm_grad_x", "grouped_gemm_grad_w",
                                        "grouped_gemm_i8"};
@@ -793,7 +846,14 @@ cudaError_t launch_kind(const GgArgs& a, int grid, size_t smem, cudaStream_t st)
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kKind, kPair>, a);
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kKind, kPair, kF32>, a);
+}
+
+template <int kKind>
+cudaError_t launch_kind(const GgArgs& a, bool pair, bool f32, int grid, size_t smem, cudaStream_t st) {
+  if (pair)
+    return f32 ? launch_as<kKind, true, true>(a, grid, smem, st) : launch_as<kKind, true, false>(a, grid, smem, st);
+  return f32 ? launch_as<kKind, false, true>(a, grid, smem, st) : launch_as<kKind, false, false>(a, grid, smem, st);
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -896,21 +956,13 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
     *unsupported = 1;
     return cudaSuccess;
   }
-  if (pair) {
-    const int grid = 2 * (int)(max_tiles < n_sms / 2 ? max_tiles : n_sms / 2);
-    switch (p.kind) {
-      case kGgForward: return launch_kind<kGgForward, true>(a, grid, smem, st);
-      case kGgGradX: return launch_kind<kGgGradX, true>(a, grid, smem, st);
-      case kGgGradW: return launch_kind<kGgGradW, true>(a, grid, smem, st);
-      default: return launch_kind<kGgInt8, true>(a, grid, smem, st);
-    }
-  }
-  const int grid = (int)(max_tiles < n_sms ? max_tiles : n_sms);
+  const int grid = pair ? 2 * (int)(max_tiles < n_sms / 2 ? max_tiles : n_sms / 2)
+                        : (int)(max_tiles < n_sms ? max_tiles : n_sms);
   switch (p.kind) {
-    case kGgForward: return launch_kind<kGgForward, false>(a, grid, smem, st);
-    case kGgGradX: return launch_kind<kGgGradX, false>(a, grid, smem, st);
-    case kGgGradW: return launch_kind<kGgGradW, false>(a, grid, smem, st);
-    default: return launch_kind<kGgInt8, false>(a, grid, smem, st);
+    case kGgForward: return launch_kind<kGgForward>(a, pair, osz == 4, grid, smem, st);
+    case kGgGradX: return launch_kind<kGgGradX>(a, pair, osz == 4, grid, smem, st);
+    case kGgGradW: return launch_kind<kGgGradW>(a, pair, osz == 4, grid, smem, st);
+    default: return launch_kind<kGgInt8>(a, pair, osz == 4, grid, smem, st);
   }
 }
 

@@ -241,7 +241,10 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, const vo
  * read into any result nor written.
  *
  * Values of each product are exact products summed in fp32 (int8: exactly, in
- * int32) and rounded once to the output type.  A row's result is computed from
+ * int32) and rounded once to the output type.  The tensor cores cut each of
+ * their additions short instead of rounding it; sums for fp32 results are taken
+ * in pieces of 640 products that are added with rounding (about 1e-6 of a sum's
+ * size in all, whatever its length).  A row's result is computed from
  * that row alone, and the same call gives the same bits again; the order of the
  * fp32 sum, and so its last bits, may change with the number of rows in the
  * call.  Groups may be
@@ -283,8 +286,8 @@ moe_status moe_grouped_gemm_grad_x(const moe_gemm_desc* desc, const void* dy, co
 
 /* Gradient of moe_grouped_gemm with respect to w:
  * dw[e][n][k] = sum_{r of e} dy[r][n] * x[r][k], zeros for an expert without
- * rows; with accumulate != 0 (fp32 only) the sum is added to what dw holds,
- * rounded once.  out_dtype is dw's.  rows = 0 is a call like any other (it
+ * rows; with accumulate != 0 (fp32 only) the sum (its pieces) is added to
+ * what dw holds.  out_dtype is dw's.  rows = 0 is a call like any other (it
  * writes zeros); more than 2^26 rows are MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_gemm_grad_w(const moe_gemm_desc* desc, const void* dy, const void* x,
                                    const int32_t* offsets, void* dw, int accumulate, void* stream);
@@ -319,7 +322,8 @@ moe_status moe_swiglu(int32_t rows, int32_t F, int32_t dtype, const void* gate_u
                       int64_t ld_h, void* stream);
 
 /* moe_swiglu straight into 8-bit rows (the rule of moe_quant_rows_i8 on the
- * fp32 values of h): what the int8 down projection reads. */
+ * fp32 values g / (1 + e^-g) * u, each step rounded): what the int8 down
+ * projection reads. */
 moe_status moe_swiglu_quant_i8(int32_t rows, int32_t F, int32_t dtype, const void* gate_up, int64_t ld_gu,
                                int8_t* q, int64_t ld_q, float* scale, void* stream);
 

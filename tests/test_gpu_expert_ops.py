@@ -561,6 +561,47 @@ def test_gradients_against_differences():
         assert abs((loss(xd, wd + e) - loss(xd, wd - e)) / (2 * step) - dw[n, i, k].item()) <= 1e-3
 
 
+@pytest.mark.parametrize("counts,N,K", [([40, 0, 33], 130, 14336), ([300, 45], 264, 5000), ([90, 20], 37, 641),
+                                        ([3, 70], 64, 1281), ([20, 31], 33, 640)])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_long_fp32_sums_keep_their_digits(counts, N, K, odd):
+    """fp32 results of long sums: off by at most 2^-23 a product within a piece of 640 of them (its additions are
+    cut short), and by a rounding for each piece: in the norm, where such errors are of random size and the partial
+    sums smaller, well below 2e-6 of the result."""
+    g = gen(28)
+    R, E = sum(counts), len(counts)
+    off = offsets_of(counts)
+
+    def result(*shape):
+        return torch.full((*shape[:-1], shape[-1] + odd), 7.0, device=DEV)[..., : shape[-1]]
+
+    x, w, dy = normal((R, K), BF16, g), normal((E, N, K), BF16, g, 0.1), normal((R, N), BF16, g)
+    out = result(R, N)
+    moe.moe_grouped_gemm(x, w, off, out)
+    ok()
+    ref, mag = ref_forward(x, w, off)
+    check(out, ref, mag * (640 + 2 + K / 640) * U)
+    assert (out.double() - ref).norm() <= 2e-6 * ref.norm()
+    wt = normal((E, K, N), BF16, g, 0.1)  # the other way round: the sums of dx run over K
+    dyk, dx = normal((R, K), BF16, g), result(R, N)
+    moe.moe_grouped_gemm_grad_x(dyk, wt, off, dx)
+    ok()
+    ref, mag = ref_forward(dyk, wt.transpose(1, 2), off)
+    check(dx, ref, mag * (640 + 2 + K / 640) * U)
+    assert (dx.double() - ref).norm() <= 2e-6 * ref.norm()
+    long = [K, 3, 0]
+    offl = offsets_of(long)
+    xl, dyl = normal((K + 3, 40), BF16, g), normal((K + 3, 72), BF16, g)
+    for accumulate in (False, True):
+        dw = result(3, 72, 40)
+        before = dw.double() if accumulate else 0
+        moe.moe_grouped_gemm_grad_w(dyl, xl, offl, dw, accumulate=accumulate)
+        ok()
+        ref, mag = ref_grad_w(dyl, xl, offl)
+        check(dw, ref + before, (mag + 7) * (640 + 2 + K / 640) * U)
+        assert (dw.double() - ref - before).norm() <= 2e-6 * (ref + before).norm()
+
+
 # ------------------------------------------------------------- row operators
 
 def ref_codes(v):
@@ -733,6 +774,9 @@ def test_swiglu_quant(R, F, extra, t):
     # a code lies within half a step of its value, and a little for the value's own error
     assert bool(((v / (amax / 127)[:, None] - q.double()).abs() <= 0.5 + 127 * (2 * rel + 2 * U)).all())
     assert bool((q.abs().amax(1) == 127).all())
+    # expf is off by 2 units of its last place, 4 U, at most; with the sum, the quotient and the product a value by
+    # 7 U; with as much again for the row's largest and two roundings a code's argument by 16 U
+    assert bool(((v / (amax / 127)[:, None] - q.double()).abs() <= 0.5 + 127 * 16 * U).all())
 
 
 # ------------------------------------------------------------- used together
