@@ -316,7 +316,8 @@ moe_status moe_quant_rows_i8(int32_t rows, int32_t K, int32_t dtype, const void*
                              void* stream);
 
 /* h[r][f] = silu(g) * u, g = gate_up[r][f], u = gate_up[r][F + f] (the order
- * of W13's rows), computed in fp32.  gate_up [rows][2F] of pitch ld_gu (0: 2F),
+ * of W13's rows), computed in fp32 (1 / (1 + e^-g) is taken as 0 where it is
+ * below 2^-126, g < -87.3).  gate_up [rows][2F] of pitch ld_gu (0: 2F),
  * h [rows][F] of pitch ld_h (0: F), both bf16 or fp16. */
 moe_status moe_swiglu(int32_t rows, int32_t F, int32_t dtype, const void* gate_up, int64_t ld_gu, void* h,
                       int64_t ld_h, void* stream);
