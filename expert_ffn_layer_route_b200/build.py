@@ -24,7 +24,10 @@ LIB = os.path.join(PKG, "libmoe_b200.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
-         "-rdc=true", "-I" + os.path.join(ROOT, "include")]
+         "-I" + os.path.join(ROOT, "include")]
+# A kernel that moves registers between its warps (setmaxnreg) has to be compiled as a whole program: relocatable
+# device code is compiled as if a function of another file could be called with the launch's registers.
+WHOLE = {"grouped_gemm.cu"}
 
 
 def nvcc() -> str:
@@ -46,7 +49,8 @@ def _stale(obj: str, src: str, hdr_mtime: float) -> bool:
 
 
 def _compile(src: str, obj: str, extra):
-    cmd = [nvcc()] + ARCH + FLAGS + list(extra) + ["-c", src, "-o", obj]
+    rdc = ["-DMOE_OWN_STATUS_WORD"] if os.path.basename(src) in WHOLE else ["-rdc=true"]
+    cmd = [nvcc()] + ARCH + FLAGS + rdc + list(extra) + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     return src, r.returncode, r.stdout + r.stderr
 

@@ -16,8 +16,14 @@
 
 namespace moe {
 
-// Sticky device status word (first error wins).  Defined in moe_api.cu.
+// Sticky device status word (first error wins).  Defined in moe_api.cu; a file
+// that is compiled by itself (build.py says which, and why) has one of its own,
+// which moe_get_last_error reads too.
+#ifdef MOE_OWN_STATUS_WORD
+static __device__ int g_status;
+#else
 extern __device__ int g_status;
+#endif
 
 __device__ __forceinline__ void set_status(int code) { atomicCAS(&g_status, 0, code); }
 

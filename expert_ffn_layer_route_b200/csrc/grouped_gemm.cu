@@ -15,9 +15,9 @@
 // at most 15 columns (31 in pairs of CTAs).
 //
 // Roles of a CTA: warp 0 brings the operands (TMA, a ring of stages), warp 1
-// issues the MMAs, 4 warps write results (grad_w 8, and one more clears the
-// ragged ends of groups); two accumulators, so that a tile's results leave under
-// the next one's products.  Measured (B200, HBM copy 6.56 TB/s, cuBLAS bf16 1.61
+// issues the MMAs, 4 warps (8 in tiles of more than 64 columns) take the sums and
+// write results, and in grad_w one more clears the ragged ends of groups; two
+// accumulators, so that one is read under the next one's products.  Measured (B200, HBM copy 6.56 TB/s, cuBLAS bf16 1.61
 // PFLOP/s in short runs, 1.37 at the power limit): 2048 x 28672 x 4096 bf16 329 us
 // (1460 TFLOP/s); 8192 ragged rows of 8 experts, the same matrices, 1.37-1.44 ms
 // (1340-1400), 1.55 at the power limit; 256 rows of 128 experts, [5760][2880],
@@ -41,28 +41,38 @@ constexpr int kChan = 128;             // channels per CTA and tile: the TMEM la
 constexpr int kLine = 128;             // bytes of the contraction per K-major block (one swizzle line)
 constexpr int kSlabBytes = 64 * 128;   // channel-major block: 64 contraction rows x 64 channels of 16 bits
 constexpr int kABlock = kChan * kLine;  // the channels' operand of a block, either way
-// The tensor cores cut their fp32 additions short (they do not round them): over
-// 3500 products a sum comes out 4e-6 off, over 9000 1.1e-5.  A 16-bit result does
-// not show it.  An fp32 one is summed in pieces, each by its own accumulator, which
-// the epilogue adds in fp32 (under 1e-6 whatever the depth; the result's lines
-// are read and written again for each, mostly in L2).  int8 sums are exact.
+// The tensor cores cut their fp32 additions short (they do not round them): left
+// to one accumulator, a sum over 3500 products comes out 4e-6 off, over 28672
+// 3e-5, over 400000 half a step of fp16.  So a sum is taken in pieces of 640
+// products, each by its own accumulator, which the epilogue adds in registers with
+// rounded fp32 additions (under 1e-6 up to some 10^5 products).  int8 sums are exact.
 constexpr int kPiece = 640;  // contraction elements (a multiple of a step's, 64 or 128)
 constexpr int kMaxStages = 12;
 constexpr int64_t kMaxTiles = (int64_t)1 << 30;
-// A warp reads the 32 TMEM lanes of its quadrant.  grad_w has two warps to a
-// quadrant, which take its 128-byte columns in turn: with few rows to a group
-// its tiles are all epilogue, and a warp spends most of a column's 600 cycles on
-// latencies (fp32 gradients of 128 experts with 64 rows each: 868 us with 4
-// warps, 793 with 8).
-constexpr int epi_warps(int kind) { return kind == kGgGradW ? 8 : 4; }
-constexpr int gg_threads(int kind) { return 32 * (2 + epi_warps(kind) + (kind == kGgGradW ? 1 : 0)); }
+// A warp reads the 32 TMEM lanes of its quadrant.  Tiles of more than 64 columns
+// have two warps to a quadrant, which take its columns in turn: the sums of 256
+// columns then fit a thread's registers, 128 of them each; and with few rows to
+// a group a grad_w tile is all epilogue, most of it latencies (fp32 gradients of
+// 128 experts with 64 rows each: 868 us with 4 warps, 793 with 8).
+constexpr int epi_warps(int kind, bool pair) { return pair || kind == kGgGradW ? 8 : 4; }
+// Warps before the epilogue's: TMA, MMA; grad_w: the clearing one and an idle one
+// too, a warpgroup, which leaves the epilogue's two some of its registers.
+constexpr int first_epi(int kind) { return kind == kGgGradW ? 4 : 2; }
+constexpr int gg_threads(int kind, bool pair) { return 32 * (first_epi(kind) + epi_warps(kind, pair)); }
+// grad_w is launched with 384 threads of 168 registers (65536 / 384, in steps of
+// 8).  Its epilogue wants more, for the sums of 256 columns next to the way out of
+// a tile of one piece; what does not fit would live in local memory, which has no
+// cache worth the name beside this shared memory (fp32 gradients of 128 experts
+// with 64 rows each: 1500 us).
+constexpr int kLaunchRegs = 168, kIssueRegs = 56, kEpiRegs = 224;
+static_assert(kIssueRegs + 2 * kEpiRegs == 3 * kLaunchRegs, "what the warpgroups have together is what they were launched with");
+constexpr int kSingleCols = 64;  // widest tile of one CTA (but grad_w)
+enum { k16, kF32Out, kF32Add };  // result: a 16-bit type, fp32, (grad_w) fp32 added to what is there
 constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of the ragged operand
 
 // Staging buffer of one epilogue warp: 32 rows x 32 channels (forward, grad_x,
-// int8; rows padded against bank conflicts), or 32 lines of 128 bytes, their
-// 16-byte pieces swizzled (grad_w).
-constexpr int kPitch16 = 80, kPitch32 = 144;
-constexpr int epi_bytes(int kind) { return kind == kGgGradW ? 32 * 128 : 5 * 1024; }
+// int8), or 32 lines of 128 bytes, their 16-byte pieces swizzled (grad_w).
+constexpr int epi_bytes(int kind, bool f32) { return kind == kGgGradW || f32 ? 32 * 128 : 32 * 64; }
 
 struct alignas(64) GgArgs {
   CUtensorMap tm_a;
@@ -183,21 +193,24 @@ __device__ __forceinline__ void st_global16(uint8_t* p, const uint4& v) {
   asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Staged lines to global memory, every lane 16 bytes of a row at a time, all
-// loads before the first store: kPieces 16-byte pieces a row, rows [0, n) of
+// Staged lines to global memory, every lane 16 bytes of a row at a time, kBatch
+// loads before their stores: kPieces 16-byte pieces a row, rows [0, n) of
 // 32, all of a row's pieces wanted.  at(row, piece): the staged address.
-template <int kPieces, typename At>
+template <int kPieces, int kBatch, typename At>
 __device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, int n, int lane, At at) {
   constexpr int kRows = 32 / kPieces;  // rows a warp stores at once
   const int piece = lane % kPieces, r0 = lane / kPieces;
-  uint4 t[kPieces];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) t[i] = lds128(at(r0 + i * kRows, piece));
   uint8_t* d = out + r0 * pitch + piece * 16;
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    if (r0 + i * kRows < n) st_global16(d, t[i]);
-    d += kRows * pitch;
+  for (int b = 0; b < kPieces; b += kBatch) {
+    uint4 t[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) t[i] = lds128(at(r0 + (b + i) * kRows, piece));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (r0 + (b + i) * kRows < n) st_global16(d, t[i]);
+      d += kRows * pitch;
+    }
   }
 }
 
@@ -217,10 +230,11 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[4]) {
 // edges (bytes [0, width) of each row), and (kAdd, fp32) sums added to what is
 // there.  Staged rows of kRowBytes, kPitch apart, their 16-byte pieces swizzled
 // or not; a lane keeps its place in the row and steps through the rows.
-template <int kVec, int kRowBytes, int kPitch, bool kSwizzled, bool kAdd>
+template <int kVec, int kRowBytes, int kPitch, bool kSwizzled, bool kAdd, int kMost>
 __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int lane) {
   constexpr int kBytes = kVec < 4 ? 4 : kVec, kWords = kBytes / 4;  // per lane and row
-  constexpr int kPieces = kRowBytes / kBytes, kRows = 32 / kPieces, kBatch = kPieces < 8 ? kPieces : 8;
+  constexpr int kPieces = kRowBytes / kBytes, kRows = 32 / kPieces;
+  constexpr int kBatch = kMost < kPieces ? kMost : kPieces;  // loads before their stores
   const int r0 = lane / kPieces, b = lane % kPieces * kBytes;
   const uint32_t s = staged + r0 * kPitch + (kSwizzled ? (((b >> 4) ^ r0) << 4 | (b & 15)) : b);
   uint8_t* d = out + r0 * pitch + b;
@@ -243,6 +257,7 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
     }
   };
   if (b + kBytes <= width) {
+    static_assert(!kSwizzled || kBatch * kRows % 8 == 0, "the swizzle goes by a row's place in its batch");
 #pragma unroll 1
     for (int i0 = 0; i0 * kRows < n; i0 += kBatch) {
       uint32_t t[kBatch][kWords];
@@ -250,7 +265,7 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
       uint8_t* p[kBatch];
       const int left = n - r0 - i0 * kRows;  // rows from this lane's first on
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {  // (a batch is a multiple of 8 rows where the swizzle counts)
+      for (int i = 0; i < kBatch; ++i) {
         lds_words((kSwizzled ? s ^ ((i * kRows & 7) << 4) : s) + (i0 + i) * kRows * kPitch, t[i]);
         p[i] = d;
         d += kRows * pitch;
@@ -293,43 +308,182 @@ __device__ __forceinline__ void store_pieces(uint8_t* out, int64_t pitch, uint32
   }
 }
 
-// rows of 32 channels, kElem bytes each (out of line: the common case stays small)
-template <int kElem, bool kInPieces>
-__device__ __noinline__ void store_rows_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
-                                            int add, int lane) {
-  constexpr int kRow = 32 * kElem, kStaged = kElem == 4 ? kPitch32 : kPitch16;
-  if (kInPieces && add) {
-    if (vec == 16)
-      store_pieces<16, kRow, kStaged, false, true>(out, pitch, staged, n, width, lane);
-    else
-      store_pieces<4, kRow, kStaged, false, true>(out, pitch, staged, n, width, lane);
-  } else if (vec == 16)
-    store_pieces<16, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
-  else if (vec == 8)
-    store_pieces<8, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
-  else if (vec == 4 || kElem == 4)
-    store_pieces<4, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
+// rows of kRow bytes (kSwizzled: lines of 128, their 16-byte pieces swizzled), values of kElem bytes (in line: a
+// call would have to save the sums that the thread still holds)
+template <int kElem, int kRow, bool kSwizzled, bool kAdd, bool kVec16, int kMost>
+__device__ __forceinline__ void store_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
+                                          int lane) {
+  if constexpr (kVec16)
+    store_pieces<16, kRow, kRow, kSwizzled, kAdd, kAdd ? 2 : kMost>(out, pitch, staged, n, width, lane);
+  else if (!kAdd && vec == 8)
+    store_pieces<8, kRow, kRow, kSwizzled, false, kMost>(out, pitch, staged, n, width, lane);
+  else if (vec >= 4 || kElem == 4)
+    store_pieces<4, kRow, kRow, kSwizzled, kAdd, 8>(out, pitch, staged, n, width, lane);
   else
-    store_pieces<2, kRow, kStaged, false, false>(out, pitch, staged, n, width, lane);
+    store_pieces<2, kRow, kRow, kSwizzled, false, 8>(out, pitch, staged, n, width, lane);
 }
 
-// lines of 128 bytes, their 16-byte pieces swizzled (in line: a call here would have to save the columns that
-// are on their way from tensor memory)
-template <bool kInPieces>
-__device__ __forceinline__ void store_lines_any(uint8_t* out, int64_t pitch, uint32_t staged, int n, int width, int vec,
-                                             int add, int lane) {
-  if (kInPieces && add && vec == 16)
-    store_pieces<16, 128, 128, true, true>(out, pitch, staged, n, width, lane);
-  else if (kInPieces && add)
-    store_pieces<4, 128, 128, true, true>(out, pitch, staged, n, width, lane);
-  else if (vec == 16)
-    store_pieces<16, 128, 128, true, false>(out, pitch, staged, n, width, lane);
-  else if (vec == 8)
-    store_pieces<8, 128, 128, true, false>(out, pitch, staged, n, width, lane);
-  else if (vec == 4)
-    store_pieces<4, 128, 128, true, false>(out, pitch, staged, n, width, lane);
-  else
-    store_pieces<2, 128, 128, true, false>(out, pitch, staged, n, width, lane);
+// grad_w's way out: 32 rows n of dw, 128 bytes of k at a time.  A thread holds
+// one row's line; through shared memory the lines leave 8 lanes to a line.
+struct LineOut {
+  uint8_t* out;    // first row and column of the warp's part of the tile
+  int64_t pitch;   // bytes
+  int n, nc;       // rows; columns of the tile that exist
+  uint8_t* stage;  // the warp's buffer
+  int dtype, vec;
+};
+
+// 32 values to the lane's line, from its 16-byte piece `at` on.
+template <bool kF32>
+__device__ __forceinline__ void put_line(const LineOut& w, int at, const uint32_t (&v)[32], int lane) {
+  uint4* line = reinterpret_cast<uint4*>(w.stage + lane * 128);
+  if constexpr (kF32) {
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      line[(at + z) ^ (lane & 7)] = make_uint4(v[4 * z], v[4 * z + 1], v[4 * z + 2], v[4 * z + 3]);
+  } else {
+    auto put = [&](int dtype) {
+      auto two = [&](int j) { return pack16(dtype, __uint_as_float(v[j]), __uint_as_float(v[j + 1])); };
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        line[(at + z) ^ (lane & 7)] = make_uint4(two(8 * z), two(8 * z + 2), two(8 * z + 4), two(8 * z + 6));
+    };
+    if (w.dtype == MOE_T_BF16)
+      put(MOE_T_BF16);
+    else
+      put(MOE_T_FP16);
+  }
+}
+
+__device__ __forceinline__ void clear_lines(const LineOut& w, int lane) {
+#pragma unroll
+  for (int z = 0; z < 8; ++z) reinterpret_cast<uint4*>(w.stage + lane * 128)[z ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
+}
+
+// The staged lines of column j0.
+template <int kOut, bool kVec16, int kMost, typename F>
+__device__ __forceinline__ void store_line(const LineOut& w, int j0, int lane, F between) {
+  constexpr bool kAdd = kOut == kF32Add;
+  constexpr int osz = kOut == k16 ? 2 : 4;
+  const uint32_t staged = smem_u32(w.stage);
+  __syncwarp();
+  const int width = min(128, (w.nc - j0) * osz);
+  if (!kAdd && kVec16 && width == 128) {
+    between();
+    store_lines<8, kMost>(w.out + j0 * osz, w.pitch, w.n, lane,
+                   [&](int r, int p) { return staged + r * 128 + ((p ^ (r & 7)) << 4); });
+  } else {
+    store_any<osz, 128, true, kAdd, kVec16, kMost>(w.out + j0 * osz, w.pitch, staged, w.n, width, w.vec, lane);
+    __syncwarp();
+    between();
+  }
+  __syncwarp();
+}
+
+// What sums will be added to, on its way to L2 while the tile's products run:
+// a lane's row, the warp's lines of 32 columns.
+__device__ __forceinline__ void prefetch_lines(const LineOut& w, int first, int step, int lane) {
+  if (lane >= w.n) return;
+  for (int j0 = first; j0 < w.nc; j0 += step)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(w.out + lane * w.pitch + j0 * 4));
+}
+
+// The accumulators as an epilogue warp takes them, one after the other.
+template <bool kPair>
+struct Accumulators {
+  uint64_t *full, *empty;
+  volatile int* abort;
+  uint32_t lanes;  // tensor-memory address of the warp's quadrant
+  int col_cap;
+  int i;  // taken so far
+
+  __device__ __forceinline__ bool take() {  // waits for the next one (false: given up)
+    const bool got = !warp_any(*abort) && warp_wait(&full[i & 1], (uint32_t)(i >> 1) & 1u);
+    if (!got) *abort = 1;
+    tc::fence_after_sync();
+    return got;
+  }
+  __device__ __forceinline__ uint32_t addr() const { return lanes + (uint32_t)((i & 1) * col_cap); }
+  __device__ __forceinline__ void release(int lane) {  // it has been read
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      if (kPair)
+        mbar_arrive_cluster_relaxed(cluster_addr(&empty[i & 1], 0));
+      else
+        mbar_arrive(&empty[i & 1]);
+    }
+    ++i;
+  }
+};
+
+// A tile's sums to registers, the pieces (of a depth of kPiece or less) added one
+// after the other: kChunks times 32 columns, from column(c) on where that is
+// below nc.  wanted: whether the warp's channels exist.  False: given up.
+template <bool kInPieces, bool kPair, int kChunks, typename Column>
+__device__ __forceinline__ bool take_sums(Accumulators<kPair>& acc, uint32_t (&sum)[kChunks][32], int depth, int nc,
+                                          bool wanted, int lane, Column column) {
+  if (!acc.take()) return false;
+  if (wanted) {
+    // (no branch between a load and its wait; what lies past the tile's columns is read somewhere inside)
+    const int last = max(acc.col_cap - 32, 0);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) tc::ld_issue32(acc.addr() + min(column(c), last), sum[c]);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) tc::ld_wait32(sum[c]);
+  }
+  acc.release(lane);
+  if constexpr (kInPieces) {
+#pragma unroll 1
+    for (int d0 = kPiece; d0 < depth; d0 += kPiece) {
+      if (!acc.take()) return false;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (!wanted || column(c) >= nc) continue;
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+          uint32_t v[16];
+          tc::ld_32x32b_x16(acc.addr() + column(c) + h, v);
+          tc::ld_wait16(v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            sum[c][h + j] = __float_as_uint(__uint_as_float(sum[c][h + j]) + __uint_as_float(v[j]));
+        }
+      }
+      acc.release(lane);
+    }
+  }
+  return true;
+}
+
+// grad_w, a tile of several pieces: the accumulators taken so far, or -1 (given up).
+template <bool kPair, int kOut, bool kVec16>
+__device__ __forceinline__ int store_by_sums(Accumulators<kPair> acc, const LineOut w, int depth, int half, bool mine, int lane) {
+  constexpr bool kF32 = kOut != k16;
+  constexpr int kPerLine = kF32 ? 32 : 64, kChunks = 4, kChunkLine = kPerLine / 32;
+  uint32_t sum[kChunks][32];
+  if (!take_sums<true, kPair, kChunks>(acc, sum, depth, w.nc, mine, lane, [&](int c) {
+        return (half + 2 * (c / kChunkLine)) * kPerLine + c % kChunkLine * 32;
+      }))
+    return -1;
+  if (mine) {
+#pragma unroll 1
+    for (int l = 0, j0 = half * kPerLine; l < kChunks / kChunkLine && j0 < w.nc; ++l, j0 += 2 * kPerLine) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)  // (registers have no index: the line's chunks by comparison)
+        if (c / kChunkLine == l) put_line<kF32>(w, c % kChunkLine * 4, sum[c], lane);
+      store_line<kOut, kVec16, 4>(w, j0, lane, [] {});
+    }
+  }
+  return acc.i;
+}
+
+// fp32 results take it by a call: in line its registers cost the tiles of one piece
+// 7% (128 experts of 64 rows 770, 825 us; a 16-bit result leaves half the bytes).
+template <bool kPair, int kOut, bool kVec16>
+__device__ __noinline__ int store_by_sums_out_of_line(Accumulators<kPair> acc, const LineOut w, int depth, int half,
+                                                      bool mine, int lane) {
+  return store_by_sums<kPair, kOut, kVec16>(acc, w, depth, half, mine, lane);
 }
 
 }  // namespace
@@ -338,18 +492,17 @@ __device__ __forceinline__ void store_lines_any(uint8_t* out, int64_t pitch, uin
 // channels: each loads its 128 channels of A and half of the columns of B, the
 // even CTA issues one MMA for both, and each keeps its 128 channels of D.  Each
 // operand byte then crosses L2 -> SM half as often as with tiles of one CTA.
-// kF32: the result is fp32, and a sum is taken kPiece products at a time.
-template <int kKind, bool kPair, bool kF32>
-__global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(const __grid_constant__ GgArgs a) {
+template <int kKind, bool kPair, int kOut, bool kVec16>
+__global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kernel(const __grid_constant__ GgArgs a) {
   constexpr bool kAChanMajor = kKind == kGgGradX || kKind == kGgGradW;  // A rows run along the channels
   constexpr bool kBChanMajor = kKind == kGgGradW;
   constexpr int kElem = kKind == kGgInt8 ? 1 : 2;
   constexpr int kDepthBlock = kLine / kElem;  // contraction elements per block
   constexpr int kDepthMma = 32 / kElem;
   constexpr int kColRound = kPair ? 32 : 16;
-  constexpr int kEpiBytes = epi_bytes(kKind), kEpiWarps = epi_warps(kKind);
+  constexpr int kEpiBytes = epi_bytes(kKind, kOut != k16), kEpiWarps = epi_warps(kKind, kPair), kFirstEpi = first_epi(kKind);
   constexpr int kTileChan = kPair ? 2 * kChan : kChan;
-  constexpr bool kInPieces = kF32 && kKind != kGgInt8;
+  constexpr bool kInPieces = kKind != kGgInt8, kF32 = kOut != k16, kAdd = kOut == kF32Add;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = uni(tid >> 5);
@@ -390,7 +543,7 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
   pdl_wait_and_trigger();
   // Group table.  Every thread loads the offsets of some experts (one round of
   // global latency for all of them), then warp 0 compacts and numbers them.
-  for (int e = tid; e < a.E; e += gg_threads(kKind)) {
+  for (int e = tid; e < a.E; e += gg_threads(kKind, kPair)) {
     const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
     int n = hi - lo, p = e;
     if (lo < 0 || hi < lo || hi > a.rows) {
@@ -472,6 +625,9 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
   // grad_w: whether a step ends inside a group of 16 contraction rows
   auto ragged = [&](int left) { return kKind == kGgGradW && left < kDepthBlock && (left & 15) != 0; };
 
+  if constexpr (kKind == kGgGradW) {
+    if (warp < kFirstEpi) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+  }
   if (warp == 0) {
     // ================================================================ TMA producer
     // (the whole warp runs the loops, one lane is elected to issue: see the MMA warp)
@@ -648,144 +804,118 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
       mbar_wait(drain, 0);
     }
     __syncwarp();
-  } else if (warp < 2 + kEpiWarps) {
+  } else if (warp >= kFirstEpi) {
+    if constexpr (kKind == kGgGradW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ================================================================ epilogue
-    const int q = warp & 3;  // TMEM lane quadrant of this warp
-    uint8_t* stage_o = epi + (warp - 2) * kEpiBytes;
+    const int q = warp & 3;              // TMEM lane quadrant of this warp
+    const int half = (warp - kFirstEpi) >> 2;    // of two warps to a quadrant: which
+    uint8_t* stage_o = epi + (warp - kFirstEpi) * kEpiBytes;
+    const uint32_t staged = smem_u32(stage_o);
     constexpr int osz = kF32 ? 4 : 2;
-    int i = 0;
+    Accumulators<kPair> acc{acc_full, acc_empty, s_abort, tmem_base + ((uint32_t)(q * 32) << 16), a.col_cap, 0};
     for (int t = unit; t < total_tiles; t += units) {
       const Tile ti = tile_at(t);
-      // (the pieces of a tile's sum come one after the other: the first is stored, the others are added)
-      for (int d0 = 0, more = 1; more; ++i) {
-        const int buf = i & 1;
-        if (warp_any(*s_abort) || !warp_wait(&acc_full[buf], (uint32_t)(i >> 1) & 1u)) {
-          *s_abort = 1;
-          break;
-        }
-        const int add = kInPieces && (d0 > 0 || a.accumulate);
-        d0 += kPiece;
-        more = kInPieces && d0 < depth_of(ti);
-        tc::fence_after_sync();
-        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.col_cap);
-        const int ch0 = ti.m0 + rank * kChan + q * 32;
-        const bool mine = ch0 < a.channels;
-        if (!mine) {
-        } else if constexpr (kKind == kGgGradW) {
-          // 32 rows n of dw, 128 bytes of k at a time: a thread holds one row's
-          // line; through shared memory the lines leave 8 lanes to a line
-          const int per_line = 128 / osz;
-          uint8_t* const o = static_cast<uint8_t*>(a.out) +
-                             ((int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0) * osz;
-          const int64_t op = a.ldo * osz;
-          const int n = min(32, a.channels - ch0);
-          const int first = (warp - 2) / 4 * per_line, step = 2 * per_line;
-          uint32_t v[32];
-          if (first < ti.nc) tc::ld_issue32(taddr + first, v);
-          for (int j0 = first; j0 < ti.nc; j0 += step) {
-            tc::ld_wait32(v);
-            uint4* line = reinterpret_cast<uint4*>(stage_o + lane * 128);
-            if (ti.n == 0) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) line[c ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
-            } else if (osz == 4) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                line[c ^ (lane & 7)] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            } else {
-              auto half_line = [&](int c0) {
-                auto two = [&](int j) {
-                  return pack16(a.out_dtype, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                };
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  line[(c0 + c) ^ (lane & 7)] = make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
-              };
-              half_line(0);
-              tc::ld_issue32(taddr + j0 + 32, v);
+      const int ch0 = ti.m0 + rank * kChan + q * 32;
+      const bool mine = ch0 < a.channels;
+      if constexpr (kKind == kGgGradW) {
+        LineOut w;
+        w.out = static_cast<uint8_t*>(a.out) +
+                ((int64_t)ti.expert * a.stride_o + (int64_t)ch0 * a.ldo + ti.c0) * osz;
+        w.pitch = a.ldo * osz;
+        w.n = min(32, a.channels - ch0);
+        w.nc = ti.nc;
+        w.stage = stage_o;
+        w.dtype = a.out_dtype;
+        w.vec = a.vec;
+        // 128-byte lines, which the two warps of a quadrant take in turn
+        constexpr int kPerLine = kF32 ? 32 : 64;
+        if (kAdd && mine) prefetch_lines(w, half * kPerLine, 2 * kPerLine, lane);
+        if (ti.n <= kPiece) {
+          // One piece: straight from the accumulator, the next line's values on their way while one leaves.  With few
+          // rows to a group the epilogue is all there is.
+          if (!acc.take()) break;
+          if (mine) {
+            const int first = half * kPerLine;
+            uint32_t v[32];
+            if (first < ti.nc) tc::ld_issue32(acc.addr() + first, v);
+#pragma unroll 1
+            for (int j0 = first; j0 < ti.nc; j0 += 2 * kPerLine) {
               tc::ld_wait32(v);
-              half_line(4);
+              if (ti.n == 0) {
+                clear_lines(w, lane);
+              } else {
+                put_line<kF32>(w, 0, v, lane);
+                if constexpr (!kF32) {
+                  tc::ld_issue32(acc.addr() + j0 + 32, v);
+                  tc::ld_wait32(v);
+                  put_line<kF32>(w, 4, v, lane);
+                }
+              }
+              // (8 loads at a time where the registers allow it)
+              store_line<kOut, kVec16, kOut == kF32Out && kVec16 ? 4 : 8>(w, j0, lane, [&] {
+                if (j0 + 2 * kPerLine < ti.nc) tc::ld_issue32(acc.addr() + j0 + 2 * kPerLine, v);
+              });
             }
-            __syncwarp();
-            const int width = min(128, (ti.nc - j0) * osz);
-            const bool wide = a.vec == 16 && width == 128 && !add;
-            // the next line's values come while this one's leave (not across a call: they arrive in registers)
-            auto issue_next = [&] {
-              if (j0 + step < ti.nc) tc::ld_issue32(taddr + j0 + step, v);
-            };
-            if (wide) {
-              issue_next();
-              const uint32_t base = smem_u32(stage_o);
-              store_lines<8>(o + j0 * osz, op, n, lane,
-                             [&](int r, int p) { return base + r * 128 + ((p ^ (r & 7)) << 4); });
-            } else {
-              store_lines_any<kInPieces>(o + j0 * osz, op, smem_u32(stage_o), n, width, a.vec, add, lane);
-              __syncwarp();
-              issue_next();
-            }
-            __syncwarp();
           }
-        } else {
-          // 32 rows x 32 channels at a time: a thread holds one channel of 32
-          // rows; through shared memory a row's channels leave side by side
-          float sw = 0.f;
-          if (kKind == kGgInt8 && ch0 + lane < a.channels)
-            sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
-          const int64_t row0 = (int64_t)ti.row0 + ti.c0;
-          const int width = min(32, a.channels - ch0) * osz;
-          uint32_t v[32];
-          tc::ld_issue32(taddr, v);
-          for (int j0 = 0; j0 < ti.nc; j0 += 32) {
-            float sx = 0.f;
-            if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
-            tc::ld_wait32(v);
-            const int n = min(32, ti.nc - j0);
+          acc.release(lane);
+          continue;
+        }
+        if constexpr (kF32)
+          acc.i = store_by_sums_out_of_line<kPair, kOut, kVec16>(acc, w, ti.n, half, mine, lane);
+        else
+          acc.i = store_by_sums<kPair, kOut, kVec16>(acc, w, ti.n, half, mine, lane);
+        if (acc.i < 0) break;
+      } else {
+        // 32 rows x 32 channels at a time: a thread holds one channel of 32
+        // rows; through shared memory a row's channels leave side by side.
+        // Two warps to a quadrant take turns at 32 rows.
+        constexpr int kHalves = kEpiWarps / 4, kChunks = (kPair ? 256 : kSingleCols) / 32 / kHalves;
+        uint32_t sum[kChunks][32];
+        if (!take_sums<kInPieces, kPair, kChunks>(acc, sum, a.depth, ti.nc, mine, lane,
+                                                  [&](int c) { return (half + kHalves * c) * 32; }))
+          break;
+        if (!mine) continue;
+        constexpr int kRow = 32 * osz;
+        float sw = 0.f;
+        if (kKind == kGgInt8 && ch0 + lane < a.channels)
+          sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
+        const int64_t row0 = (int64_t)ti.row0 + ti.c0;
+        const int width = min(32, a.channels - ch0) * osz;
+        const int64_t op = a.ldo * osz;
+#pragma unroll 1
+        for (int l = 0, j0 = half * 32; l < kChunks && j0 < ti.nc; ++l, j0 += 32 * kHalves) {
+          float sx = 0.f;
+          if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
+          const int n = min(32, ti.nc - j0);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {  // (registers have no index: the chunk by comparison)
+            if (c != l) continue;
 #pragma unroll
             for (int g = 0; g < 32; g += 8) {
               if (g >= n) break;
 #pragma unroll
               for (int j = g; j < g + 8; ++j) {
-                float f = __uint_as_float(v[j]);
-                if constexpr (kKind == kGgInt8) f = (float)(int)v[j] * (__shfl_sync(0xffffffffu, sx, j) * sw);
-                if (osz == 4)
-                  *reinterpret_cast<float*>(stage_o + j * kPitch32 + lane * 4) = f;
+                float f = __uint_as_float(sum[c][j]);
+                if constexpr (kKind == kGgInt8) f = (float)(int)sum[c][j] * (__shfl_sync(0xffffffffu, sx, j) * sw);
+                if constexpr (osz == 4)
+                  *reinterpret_cast<float*>(stage_o + j * kRow + lane * 4) = f;
                 else
-                  *reinterpret_cast<uint16_t*>(stage_o + j * kPitch16 + lane * 2) = (uint16_t)pack16(a.out_dtype, f, 0.f);
+                  *reinterpret_cast<uint16_t*>(stage_o + j * kRow + lane * 2) = (uint16_t)pack16(a.out_dtype, f, 0.f);
               }
             }
-            __syncwarp();
-            // the next rows' values come while these leave (not across a call: they arrive in registers)
-            const bool next = j0 + 32 < ti.nc;
-            const bool wide = a.vec == 16 && width == 32 * osz && !add;
-            if (next && wide) tc::ld_issue32(taddr + j0 + 32, v);
-            uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
-            const int64_t op = a.ldo * osz;
-            const uint32_t base = smem_u32(stage_o);
-            if (!wide) {
-              store_rows_any<osz, kInPieces>(o, op, base, n, width, a.vec, add, lane);
-              __syncwarp();
-              if (next) tc::ld_issue32(taddr + j0 + 32, v);
-            } else if (osz == 4) {
-              store_lines<8>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch32 + p * 16; });
-            } else {
-              store_lines<4>(o, op, n, lane, [&](int r, int p) { return base + r * kPitch16 + p * 16; });
-            }
-            __syncwarp();
           }
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (kPair)
-            mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
+          __syncwarp();
+          uint8_t* o = static_cast<uint8_t*>(a.out) + ((row0 + j0) * a.ldo + ch0) * osz;
+          if (kVec16 && width == kRow)
+            store_lines<kRow / 16, 4>(o, op, n, lane, [&](int r, int p) { return staged + r * kRow + p * 16; });
           else
-            mbar_arrive(&acc_empty[buf]);
+            store_any<osz, kRow, false, false, kVec16, 2>(o, op, staged, n, width, a.vec, lane);
+          __syncwarp();
         }
       }
-      if (warp_any(*s_abort)) break;
     }
   }
-  if (kKind == kGgGradW && warp == 2 + kEpiWarps) {
+  if (kKind == kGgGradW && warp == 2) {
     // ================================================================ clears the ragged stages
     uint32_t cnt = 0, uses = 0;
     for (int t = unit; t < total_tiles; t += units) {
@@ -820,16 +950,24 @@ __global__ void __launch_bounds__(gg_threads(kKind), 1) grouped_gemm_kernel(cons
 // ------------------------------------------------------------------ host side
 namespace {
 
-template <int kKind, bool kPair, bool kF32>
+template <int kKind, bool kPair, int kOut, bool kVec16>
 cudaError_t launch_as(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
-  cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind, kPair, kF32>>(smem);
+  cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind, kPair, kOut, kVec16>>(smem);
   if (err != cudaSuccess) return err;
+  if (kKind == kGgGradW) {  // a warp would wait for registers for good if the compiler had given it fewer than that
+    static const bool as_planned = [] {
+      cudaFuncAttributes at;
+      return cudaFuncGetAttributes(&at, grouped_gemm_kernel<kKind, kPair, kOut, kVec16>) == cudaSuccess &&
+             at.numRegs == kLaunchRegs;
+    }();
+    if (!as_planned) return cudaErrorLaunchOutOfResources;
+  }
   static const char* const names[4] = {"grouped_gemm", "grouped_gemm_grad_x", "grouped_gemm_grad_w",
                                        "grouped_gemm_i8"};
   ProfScope prof(names[kKind], st);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(gg_threads(kKind));
+  cfg.blockDim = dim3(gg_threads(kKind, kPair));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -846,19 +984,37 @@ cudaError_t launch_as(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kKind, kPair, kF32>, a);
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kKind, kPair, kOut, kVec16>, a);
+}
+
+template <int kKind, bool kPair, int kOut>
+cudaError_t launch_vec(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
+  return a.vec == 16 ? launch_as<kKind, kPair, kOut, true>(a, grid, smem, st)
+                     : launch_as<kKind, kPair, kOut, false>(a, grid, smem, st);
+}
+
+template <int kKind, bool kPair>
+cudaError_t launch_out(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
+  if (a.out_dtype != MOE_T_FP32) return launch_vec<kKind, kPair, k16>(a, grid, smem, st);
+  if constexpr (kKind == kGgGradW)
+    if (a.accumulate) return launch_vec<kKind, kPair, kF32Add>(a, grid, smem, st);
+  return launch_vec<kKind, kPair, kF32Out>(a, grid, smem, st);
 }
 
 template <int kKind>
-cudaError_t launch_kind(const GgArgs& a, bool pair, bool f32, int grid, size_t smem, cudaStream_t st) {
-  if (pair)
-    return f32 ? launch_as<kKind, true, true>(a, grid, smem, st) : launch_as<kKind, true, false>(a, grid, smem, st);
-  return f32 ? launch_as<kKind, false, true>(a, grid, smem, st) : launch_as<kKind, false, false>(a, grid, smem, st);
+cudaError_t launch_kind(const GgArgs& a, bool pair, int grid, size_t smem, cudaStream_t st) {
+  return pair ? launch_out<kKind, true>(a, grid, smem, st) : launch_out<kKind, false>(a, grid, smem, st);
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
+
+cudaError_t take_grouped_gemm_status(int* status) {
+  const int zero = 0;
+  const cudaError_t err = cudaMemcpyFromSymbol(status, g_status, sizeof(int));
+  return err != cudaSuccess || *status == 0 ? err : cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
+}
 
 cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max, cudaStream_t st,
                                 int* unsupported) {
@@ -921,7 +1077,7 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   a.stage_bytes = a.blocks * (kABlock + a.b_block);
   a.tmem_cols = cap < 32 ? 64 : 2 * cap;  // (the epilogue reads 32 columns at a time)
   const size_t table = (size_t)(p.E + 1) * sizeof(Group);
-  const size_t fixed_bytes = 1024 + epi_warps(p.kind) * epi_bytes(p.kind) + (4 * kMaxStages + 8) * 8 + 32 + table;
+  const size_t fixed_bytes = 1024 + epi_warps(p.kind, pair) * epi_bytes(p.kind, osz == 4) + (4 * kMaxStages + 8) * 8 + 32 + table;
   int stages = (smem_max - (int)fixed_bytes) / a.stage_bytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) {
@@ -959,10 +1115,10 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
   const int grid = pair ? 2 * (int)(max_tiles < n_sms / 2 ? max_tiles : n_sms / 2)
                         : (int)(max_tiles < n_sms ? max_tiles : n_sms);
   switch (p.kind) {
-    case kGgForward: return launch_kind<kGgForward>(a, pair, osz == 4, grid, smem, st);
-    case kGgGradX: return launch_kind<kGgGradX>(a, pair, osz == 4, grid, smem, st);
-    case kGgGradW: return launch_kind<kGgGradW>(a, pair, osz == 4, grid, smem, st);
-    default: return launch_kind<kGgInt8>(a, pair, osz == 4, grid, smem, st);
+    case kGgForward: return launch_kind<kGgForward>(a, pair, grid, smem, st);
+    case kGgGradX: return launch_kind<kGgGradX>(a, pair, grid, smem, st);
+    case kGgGradW: return launch_kind<kGgGradW>(a, pair, grid, smem, st);
+    default: return launch_kind<kGgInt8>(a, pair, grid, smem, st);
   }
 }
 

@@ -41,6 +41,9 @@ struct GroupedProblem {
 cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max, cudaStream_t st,
                                 int* unsupported);
 
+// The status word of these kernels, and 0 to it.
+cudaError_t take_grouped_gemm_status(int* status);
+
 // The same products (forward, int8) for few rows: csrc/grouped_gemv.cu, and
 // whether that kernel is the faster one.
 bool grouped_gemv_pays(const GroupedProblem& p, int n_sms);

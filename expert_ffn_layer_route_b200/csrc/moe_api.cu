@@ -17,6 +17,7 @@
 
 #include "devinfo.cuh"
 #include "ffn_gemm_tc.cuh"
+#include "grouped_gemm.cuh"
 
 namespace moe {
 
@@ -521,6 +522,9 @@ moe_status moe_get_last_error(void) {
   if (cudaMemcpyFromSymbol(&v, moe::g_status, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
   const int zero = 0;
   if (cudaMemcpyToSymbol(moe::g_status, &zero, sizeof(int)) != cudaSuccess) return MOE_ERR_CUDA;
+  int grouped = 0;
+  if (moe::take_grouped_gemm_status(&grouped) != cudaSuccess) return MOE_ERR_CUDA;
+  if (v == 0) v = grouped;
   return static_cast<moe_status>(v);
 }
 

@@ -242,9 +242,11 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, const vo
  *
  * Values of each product are exact products summed in fp32 (int8: exactly, in
  * int32) and rounded once to the output type.  The tensor cores cut each of
- * their additions short instead of rounding it; sums for fp32 results are taken
- * in pieces of 640 products that are added with rounding (about 1e-6 of a sum's
- * size in all, whatever its length).  A row's result is computed from
+ * their additions short instead of rounding it; so a sum is taken in pieces of
+ * 640 products, which are added with rounding.  In all it is off by about 1e-6
+ * of its size up to some 10^5 products; then the pieces' roundings show, 2^-24
+ * each, which add up with the square root of their number (2^21 products: under
+ * 4e-6).  A row's result is computed from
  * that row alone, and the same call gives the same bits again; the order of the
  * fp32 sum, and so its last bits, may change with the number of rows in the
  * call.  Groups may be
@@ -286,7 +288,7 @@ moe_status moe_grouped_gemm_grad_x(const moe_gemm_desc* desc, const void* dy, co
 
 /* Gradient of moe_grouped_gemm with respect to w:
  * dw[e][n][k] = sum_{r of e} dy[r][n] * x[r][k], zeros for an expert without
- * rows; with accumulate != 0 (fp32 only) the sum (its pieces) is added to
+ * rows; with accumulate != 0 (fp32 only) the sum is added to
  * what dw holds.  out_dtype is dw's.  rows = 0 is a call like any other (it
  * writes zeros); more than 2^26 rows are MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_gemm_grad_w(const moe_gemm_desc* desc, const void* dy, const void* x,

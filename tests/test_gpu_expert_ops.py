@@ -971,3 +971,55 @@ def test_profile_names_the_kernels():
         moe.moe_profile_enable(False)
     assert set(names) == {"grouped_gemm", "grouped_gemm_grad_x", "grouped_gemm_grad_w", "grouped_gemm_i8", "swiglu",
                           "swiglu_grad", "swiglu_quant_i8"}
+
+
+# ------------------------------------------------- long sums of 16-bit results
+
+@pytest.mark.parametrize("t", [BF16, FP16], ids=str)
+@pytest.mark.parametrize("D", [4500, 28672])
+@pytest.mark.parametrize("counts,N", [([40, 0, 33], 130), ([300, 45], 264)])
+def test_16_bit_results_of_long_sums_are_those_of_the_rounded_sum(t, D, counts, N):
+    """A sum that is off by d of its size turns a rounding over where it lies within d of a border between two
+    steps: a share of 2 d / step of the values, each by one step, so sqrt(2 d step) in the norm; step is
+    finfo.eps at most, and d 2e-6, as for fp32 results."""
+    g = gen(29)
+    bound = (2 * 2e-6 * torch.finfo(t).eps) ** 0.5
+    R, E = sum(counts), len(counts)
+    off = offsets_of(counts)
+
+    def near(got, ref):
+        want = ref.to(t).double()
+        assert (got.double() - want).norm() <= bound * want.norm()
+
+    x, w, out = normal((R, D), t, g), normal((E, N, D), t, g, 0.1), torch.empty(R, N, dtype=t, device=DEV)
+    moe.moe_grouped_gemm(x, w, off, out)
+    ok()
+    near(out, ref_forward(x, w, off)[0])
+    dy, wt, dx = normal((R, D), t, g), normal((E, D, N), t, g, 0.1), torch.empty(R, N, dtype=t, device=DEV)
+    moe.moe_grouped_gemm_grad_x(dy, wt, off, dx)
+    ok()
+    near(dx, ref_forward(dy, wt.transpose(1, 2), off)[0])
+    offl = offsets_of([D - 7, 0, 100])
+    dyl, xl = normal((D + 93, N), t, g, 0.1), normal((D + 93, 72), t, g)
+    dw = torch.empty(3, N, 72, dtype=t, device=DEV)
+    moe.moe_grouped_gemm_grad_w(dyl, xl, offl, dw)
+    ok()
+    near(dw, ref_grad_w(dyl, xl, offl)[0])
+
+
+@pytest.mark.parametrize("ot", [FP16, BF16, FP32], ids=str)
+def test_grad_w_of_a_very_long_group(ot):
+    """2^21 rows of one sign: off by at most 2^-23 a product within a piece of 640, and by a rounding for each piece;
+    fp32 sums of 3300 pieces stay within 4e-6 (a random walk of roundings of 2^-25 each, twice over)."""
+    g = gen(30)
+    R = 1 << 21
+    dy, x = (torch.empty(R, 32, dtype=FP16, device=DEV) for _ in range(2))
+    for m in (dy, x):
+        m.copy_((torch.rand(R, 32, generator=g, device=DEV) + 1) * 2.0 ** -7)
+    dw = torch.empty(1, 32, 32, dtype=ot, device=DEV)
+    moe.moe_grouped_gemm_grad_w(dy, x, offsets_of([R]), dw)
+    ok()
+    ref, mag = ref_grad_w(dy, x, offsets_of([R]))
+    check(dw, ref, mag * (640 + 2 + R / 640) * U)
+    if ot == FP32:
+        assert (dw.double() - ref).norm() <= 4e-6 * ref.norm()
