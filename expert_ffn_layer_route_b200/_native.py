@@ -265,6 +265,8 @@ def _pitch(shape, stride, rows, cols, where, name) -> int:
         _refuse(where, f"{name} has shape {tuple(shape)}, ({rows}, {cols}) is wanted")
     if stride[1] != 1 and cols > 1:
         _refuse(where, f"{name}'s rows are not contiguous")
+    if rows > 1 and stride[0] < cols:  # (an expanded tensor: 0, which C would read as "not given")
+        _refuse(where, f"{name}'s rows overlap (a copy by contiguous() would not)")
     return stride[0] if rows > 1 else (cols + 15) & -16
 
 
@@ -296,7 +298,11 @@ def _gemm_desc(where, w_name, w, w_stride, w_type, x_name, x, x_stride, x_type, 
     ld_y = _pitch(y, y_stride, R, N, where, y_name)
     if w_stride[2] != 1 and K > 1:
         _refuse(where, f"{w_name}'s rows are not contiguous")
+    if N > 1 and w_stride[1] < K:
+        _refuse(where, f"{w_name}'s rows overlap (a copy by contiguous() would not)")
     ld_w = w_stride[1] if N > 1 else (K + 15) & -16
+    if M > 1 and w_stride[0] < (N - 1) * ld_w + K:
+        _refuse(where, f"{w_name}'s matrices overlap (a slot_map says which experts share a matrix)")
     d = GemmDesc(R, E, N, K, t, to, M, ld_x, ld_y, ld_w, w_stride[0] if M > 1 else N * ld_w)
     return d, ctypes.addressof(d), R, E, M, N
 

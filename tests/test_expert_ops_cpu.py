@@ -183,3 +183,46 @@ def test_python_calls_check_shapes_types_and_places():
     assert "scale" in _refused(moe.moe_swiglu_quant_i8, gu, xq, sx[:2])
     assert "CUDA" in _refused(moe.moe_swiglu_grad, gu, x, gu)
     assert "shape" in _refused(moe.moe_swiglu_grad, gu, x, _t(4, 30))
+
+
+def _rows_expanded(t):
+    return t[:1].expand_as(t)
+
+
+def test_expanded_tensors_are_refused():
+    """A tensor expanded along its rows, or along the experts, has a pitch of 0, which the C calls read as "not
+    given": every matrix argument of every call."""
+    x, w, off, out = _t(4, 16), _t(2, 8, 16), torch.zeros(3, dtype=torch.int32), _t(4, 8)
+    w_rows = w[:, :1].expand(2, 8, 16)
+    w_experts = w[:1].expand(2, 8, 16)
+    slots = torch.zeros(2, dtype=torch.int32)
+    xq, wq = _t(4, 16, dtype=torch.int8), _t(2, 8, 16, dtype=torch.int8)
+    sx, sw, gu = torch.zeros(4), torch.zeros(2, 8), _t(4, 32)
+    e = _rows_expanded
+    fwd, gx, gw, i8 = (moe.moe_grouped_gemm, moe.moe_grouped_gemm_grad_x, moe.moe_grouped_gemm_grad_w,
+                       moe.moe_grouped_gemm_i8)
+    for f, args in (
+        (fwd, (e(x), w, off, out)), (fwd, (x, w_rows, off, out)), (fwd, (x, w_experts, off, out)),
+        (fwd, (x, w, off, e(out))), (fwd, (x, w_experts, off, out, slots)),
+        (gx, (e(out), w, off, x)), (gx, (out, w_rows, off, x)), (gx, (out, w_experts, off, x)), (gx, (out, w, off, e(x))),
+        (gw, (e(out), x, off, w)), (gw, (out, e(x), off, w)), (gw, (out, x, off, w_rows)), (gw, (out, x, off, w_experts)),
+        (i8, (e(xq), sx, wq, sw, off, out)), (i8, (xq, sx, wq[:, :1].expand(2, 8, 16), sw, off, out)),
+        (i8, (xq, sx, wq[:1].expand(2, 8, 16), sw, off, out)), (i8, (xq, sx, wq, sw, off, e(out))),
+        (moe.moe_quant_rows_i8, (e(x), xq, sx)), (moe.moe_quant_rows_i8, (x, e(xq), sx)),
+        (moe.moe_quant_rows_i8, (e(x), xq, sx, torch.zeros(4, dtype=torch.int32))),
+        (moe.moe_swiglu, (e(gu), x)), (moe.moe_swiglu, (gu, e(x))),
+        (moe.moe_swiglu_quant_i8, (e(gu), xq, sx)), (moe.moe_swiglu_quant_i8, (gu, e(xq), sx)),
+        (moe.moe_swiglu_grad, (e(gu), x, gu)), (moe.moe_swiglu_grad, (gu, e(x), gu)), (moe.moe_swiglu_grad, (gu, x, e(gu))),
+    ):
+        assert "overlap" in _refused(f, *args)
+    # the gradient behind a sum over rows
+    row = torch.ones(4, 8, requires_grad=True)
+    row.sum(0).backward(torch.ones(8))
+    assert "overlap" in _refused(gx, torch.ones(8).bfloat16().expand(4, 8), w, off, x)
+    # pitches that are too small, and matrices that lie over one another
+    assert "overlap" in _refused(fwd, torch.zeros(100).bfloat16().as_strided((4, 16), (8, 1)), w, off, out)
+    assert "overlap" in _refused(fwd, x, torch.zeros(400).bfloat16().as_strided((2, 8, 16), (64, 16, 1)), off, out)
+    # one row, one matrix, one column: their strides mean nothing
+    one = _t(1, 16)
+    assert "CUDA" in _refused(fwd, one.as_strided((1, 16), (0, 1)), w, off, _t(1, 8).as_strided((1, 8), (0, 1)))
+    assert "CUDA" in _refused(fwd, x, w[:1].as_strided((1, 8, 16), (0, 16, 1)), off[:2], out)
