@@ -278,7 +278,8 @@ def _vector(t, n, dtype, where, name):
 @functools.lru_cache(maxsize=1024)
 def _gemm_desc(where, w_name, w, w_stride, w_type, x_name, x, x_stride, x_type, y_name, y, y_stride, y_type, off,
                off_stride, off_type, by_slots, a_type, b_type, out_type):
-    """(description, its address, rows, experts, matrices, N) of a grouped product: w [M][N][K], x [R][K],
+    """(description, its address, rows, experts, matrices, N) of a grouped product.  The caller holds the description
+    itself until its call is over (two threads may both make one, and only one of them is kept).  w [M][N][K], x [R][K],
     y [R][N] and offsets [E + 1], by their shapes, strides and types; a_type, b_type, out_type: the types of the
     two operands and of the result."""
     if len(w) != 3:
@@ -338,9 +339,9 @@ def moe_grouped_gemm(x, w, offsets, out, slot_map=None, stream=None):
     where = "moe_grouped_gemm"
     if _torch is None:
         _setup()
-    _, d, _, E, _, _ = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "x", x.shape, x.stride(), x.dtype, "out",
-                                  out.shape, out.stride(), out.dtype, offsets.shape, offsets.stride(), offsets.dtype,
-                                  slot_map is not None, x.dtype, w.dtype, out.dtype)
+    desc, d, _, E, _, _ = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "x", x.shape, x.stride(), x.dtype,
+                                     "out", out.shape, out.stride(), out.dtype, offsets.shape, offsets.stride(),
+                                     offsets.dtype, slot_map is not None, x.dtype, w.dtype, out.dtype)
     if slot_map is not None:
         _vector(slot_map, E, _torch.int32, where, "slot_map")
     _call(where, _one_gpu(where, x, w, offsets, out, slot_map), _LIB.moe_grouped_gemm, stream, d, x.data_ptr(),
@@ -352,9 +353,9 @@ def moe_grouped_gemm_grad_x(dy, w, offsets, dx, slot_map=None, stream=None):
     where = "moe_grouped_gemm_grad_x"
     if _torch is None:
         _setup()
-    _, d, _, E, _, _ = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "dx", dx.shape, dx.stride(), dx.dtype,
-                                  "dy", dy.shape, dy.stride(), dy.dtype, offsets.shape, offsets.stride(),
-                                  offsets.dtype, slot_map is not None, dy.dtype, w.dtype, dx.dtype)
+    desc, d, _, E, _, _ = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "dx", dx.shape, dx.stride(), dx.dtype,
+                                     "dy", dy.shape, dy.stride(), dy.dtype, offsets.shape, offsets.stride(),
+                                     offsets.dtype, slot_map is not None, dy.dtype, w.dtype, dx.dtype)
     if slot_map is not None:
         _vector(slot_map, E, _torch.int32, where, "slot_map")
     _call(where, _one_gpu(where, dy, w, offsets, dx, slot_map), _LIB.moe_grouped_gemm_grad_x, stream, d,
@@ -366,9 +367,9 @@ def moe_grouped_gemm_grad_w(dy, x, offsets, dw, accumulate=False, stream=None):
     where = "moe_grouped_gemm_grad_w"
     if _torch is None:
         _setup()
-    _, d, _, _, _, _ = _gemm_desc(where, "dw", dw.shape, dw.stride(), dw.dtype, "x", x.shape, x.stride(), x.dtype,
-                                  "dy", dy.shape, dy.stride(), dy.dtype, offsets.shape, offsets.stride(),
-                                  offsets.dtype, False, dy.dtype, x.dtype, dw.dtype)
+    desc, d, _, _, _, _ = _gemm_desc(where, "dw", dw.shape, dw.stride(), dw.dtype, "x", x.shape, x.stride(), x.dtype,
+                                     "dy", dy.shape, dy.stride(), dy.dtype, offsets.shape, offsets.stride(),
+                                     offsets.dtype, False, dy.dtype, x.dtype, dw.dtype)
     _call(where, _one_gpu(where, dy, x, offsets, dw), _LIB.moe_grouped_gemm_grad_w, stream, d, dy.data_ptr(),
           x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), 1 if accumulate else 0)
 
@@ -378,9 +379,9 @@ def moe_grouped_gemm_i8(x, x_scale, w, w_scale, offsets, out, slot_map=None, str
     where = "moe_grouped_gemm_i8"
     if _torch is None:
         _setup()
-    _, d, R, E, M, N = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "x", x.shape, x.stride(), x.dtype, "out",
-                                  out.shape, out.stride(), out.dtype, offsets.shape, offsets.stride(), offsets.dtype,
-                                  slot_map is not None, x.dtype, w.dtype, out.dtype)
+    desc, d, R, E, M, N = _gemm_desc(where, "w", w.shape, w.stride(), w.dtype, "x", x.shape, x.stride(), x.dtype,
+                                     "out", out.shape, out.stride(), out.dtype, offsets.shape, offsets.stride(),
+                                     offsets.dtype, slot_map is not None, x.dtype, w.dtype, out.dtype)
     _vector(x_scale, R, _torch.float32, where, "x_scale")
     if w_scale.shape != (M, N) or w_scale.dtype != _torch.float32 or not w_scale.is_contiguous():
         _refuse(where, f"w_scale has to be a contiguous float32 tensor of shape ({M}, {N})")

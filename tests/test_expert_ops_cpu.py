@@ -226,3 +226,57 @@ def test_expanded_tensors_are_refused():
     one = _t(1, 16)
     assert "CUDA" in _refused(fwd, one.as_strided((1, 16), (0, 1)), w, off, _t(1, 8).as_strided((1, 8), (0, 1)))
     assert "CUDA" in _refused(fwd, x, w[:1].as_strided((1, 8, 16), (0, 16, 1)), off[:2], out)
+
+
+def test_a_description_lives_until_c_has_read_it(monkeypatch):
+    """Two threads that ask for the description of the same sizes at once: only one of the two is kept by the cache,
+    and the other has to live through its own call all the same."""
+    import gc
+    import threading
+
+    n = moe._native
+    if n._torch is None:
+        n._setup()
+    both, live, calls = threading.Barrier(2), set(), []
+    pitch = n._pitch
+
+    class Desc(moe.GemmDesc):
+        def __init__(self, *a):
+            super().__init__(*a)
+            live.add(ctypes.addressof(self))
+
+        def __del__(self):
+            live.discard(ctypes.addressof(self))
+
+    def slow_pitch(*a):  # (inside the function that the cache holds the answers of: both threads miss)
+        if a[-1] == "x":
+            both.wait(60)
+        return pitch(*a)
+
+    def c_call(d, *a):
+        both.wait(60)
+        gc.collect()
+        calls.append(d in live)
+        both.wait(60)
+        return 0
+
+    class Lib:
+        moe_grouped_gemm = moe_grouped_gemm_grad_x = moe_grouped_gemm_grad_w = moe_grouped_gemm_i8 = staticmethod(c_call)
+
+    for name, value in (("GemmDesc", Desc), ("_pitch", slow_pitch), ("_LIB", Lib), ("_one_gpu", lambda *a: 0),
+                        ("_raw_stream", lambda i: 0), ("_current", lambda: 0)):
+        monkeypatch.setattr(n, name, value)
+    x, w, off, out = _t(4, 72), _t(2, 56, 72), torch.zeros(3, dtype=torch.int32), _t(4, 56)
+    q, wq = _t(4, 72, dtype=torch.int8), _t(2, 56, 72, dtype=torch.int8)
+    for f, args in ((moe.moe_grouped_gemm, (x, w, off, out)), (moe.moe_grouped_gemm_grad_x, (out, w, off, x)),
+                    (moe.moe_grouped_gemm_grad_w, (out, x, off, w)),
+                    (moe.moe_grouped_gemm_i8, (q, torch.zeros(4), wq, torch.zeros(2, 56), off, out))):
+        n._gemm_desc.cache_clear()
+        calls.clear()
+        threads = [threading.Thread(target=f, args=args) for _ in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join(120)
+        assert calls == [True, True], f.__name__
+    n._gemm_desc.cache_clear()
