@@ -22,9 +22,11 @@ struct Pitch {
   int64_t x, y, w, stride;
 };
 
-moe_status check_gemm(const moe_gemm_desc* d, bool int8, Pitch* t) {
+// own_matrices: expert e's matrix is matrix e of w (no slot_map says otherwise)
+moe_status check_gemm(const moe_gemm_desc* d, bool int8, bool own_matrices, Pitch* t) {
   if (!d) return MOE_ERR_INVALID_ARG;
   if (d->rows < 0 || d->n_experts <= 0 || d->N <= 0 || d->K <= 0 || d->n_physical < 0) return MOE_ERR_INVALID_ARG;
+  if (own_matrices && d->n_physical && d->n_physical < d->n_experts) return MOE_ERR_INVALID_ARG;
   if (int8 ? d->dtype != MOE_T_INT8 : !is16(d->dtype)) return MOE_ERR_INVALID_ARG;
   if (!is16(d->out_dtype) && d->out_dtype != MOE_T_FP32) return MOE_ERR_INVALID_ARG;
   if (d->n_experts > 1024 || d->N > kMaxExtent || d->K > kMaxExtent || (int8 && d->K > kMaxDepthI8) ||
@@ -85,7 +87,7 @@ extern "C" {
 moe_status moe_grouped_gemm(const moe_gemm_desc* desc, const void* x, const void* w, const int32_t* slot_map,
                             const int32_t* offsets, void* out, void* stream) {
   Pitch t;
-  moe_status s = check_gemm(desc, false, &t);
+  moe_status s = check_gemm(desc, false, !slot_map, &t);
   if (s != MOE_OK || desc->rows == 0) return s;
   if (!operand(x, t.x, 2) || !operand(w, t.w, 2) || t.stride % 8 || !offsets || !out ||
       !on(out, size_of(desc->out_dtype)))
@@ -105,7 +107,7 @@ moe_status moe_grouped_gemm(const moe_gemm_desc* desc, const void* x, const void
 moe_status moe_grouped_gemm_grad_x(const moe_gemm_desc* desc, const void* dy, const void* w,
                                    const int32_t* slot_map, const int32_t* offsets, void* dx, void* stream) {
   Pitch t;
-  moe_status s = check_gemm(desc, false, &t);
+  moe_status s = check_gemm(desc, false, !slot_map, &t);
   if (s != MOE_OK || desc->rows == 0) return s;
   if (!operand(dy, t.y, 2) || !operand(w, t.w, 2) || t.stride % 8 || !offsets || !dx ||
       !on(dx, size_of(desc->out_dtype)))
@@ -125,7 +127,7 @@ moe_status moe_grouped_gemm_grad_x(const moe_gemm_desc* desc, const void* dy, co
 moe_status moe_grouped_gemm_grad_w(const moe_gemm_desc* desc, const void* dy, const void* x,
                                    const int32_t* offsets, void* dw, int accumulate, void* stream) {
   Pitch t;
-  moe_status s = check_gemm(desc, false, &t);
+  moe_status s = check_gemm(desc, false, false, &t);
   if (s != MOE_OK) return s;
   if (accumulate && desc->out_dtype != MOE_T_FP32) return MOE_ERR_INVALID_ARG;
   if (desc->rows > kMaxGradRows) return MOE_ERR_UNSUPPORTED;
@@ -148,7 +150,7 @@ moe_status moe_grouped_gemm_i8(const moe_gemm_desc* desc, const int8_t* x, const
                                const float* w_scale, const int32_t* slot_map, const int32_t* offsets, void* out,
                                void* stream) {
   Pitch t;
-  moe_status s = check_gemm(desc, true, &t);
+  moe_status s = check_gemm(desc, true, !slot_map, &t);
   if (s != MOE_OK || desc->rows == 0) return s;
   if (!operand(x, t.x, 1) || !operand(w, t.w, 1) || t.stride % 16 || !offsets || !out ||
       !on(out, size_of(desc->out_dtype)) || !x_scale || !on(x_scale, 4) || !w_scale || !on(w_scale, 4))

@@ -266,7 +266,7 @@ typedef struct {
   int32_t N, K;        /* an expert's matrix is [N][K]; 1 <= N, K <= 2^20 (int8: K <= 131071) */
   int32_t dtype;       /* moe_dtype of the operands: bf16 or fp16 (moe_grouped_gemm_i8: int8) */
   int32_t out_dtype;   /* moe_dtype of the result: bf16, fp16 or fp32 */
-  int32_t n_physical;  /* matrices that w holds (0: n_experts) */
+  int32_t n_physical;  /* matrices that w holds (0: n_experts; fewer than that only with a slot_map) */
   int64_t ld_x;        /* row pitch of x, codes, dx [rows][K] in elements (0: K) */
   int64_t ld_y;        /* row pitch of out, dy [rows][N] in elements (0: N) */
   int64_t ld_w;        /* row pitch of w, dw [N][K] in elements (0: K) */

@@ -280,3 +280,14 @@ def test_a_description_lives_until_c_has_read_it(monkeypatch):
             t.join(120)
         assert calls == [True, True], f.__name__
     n._gemm_desc.cache_clear()
+
+
+def test_fewer_matrices_than_experts_need_a_slot_map():
+    """Without one expert e's matrix is matrix e, which has to exist."""
+    L, off = moe.lib(), P
+    for d in (_desc(n_experts=4, n_physical=3), _desc(n_experts=4, n_physical=1)):
+        assert _forward(d) == _grad_x(d) == INVALID
+    assert _int8(_desc(dtype=3, n_experts=4, n_physical=3)) == INVALID
+    assert _forward(_desc(rows=0, n_experts=4, n_physical=3)) == INVALID
+    # (with one: nothing to do, and no complaint)
+    assert L.moe_grouped_gemm(ctypes.byref(_desc(rows=0, n_experts=4, n_physical=3)), P, P, P, off, P, None) == 0
