@@ -217,10 +217,14 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
 // are read once whatever the routing.
 template <int kType, bool kSplit>
 __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(const GemvArgs a) {
-  __shared__ int s_n, s_phys;
+  // The group that starts at the block's row: expert, rows and matrix in one word, the lowest expert's if offsets
+  // that go back and forth claim the row for several.
+  constexpr int kPhysBits = 31, kRowBits = 8;
+  constexpr unsigned long long kNone = ~0ull;
+  __shared__ unsigned long long s_group;
   const int tid = threadIdx.x, lane = tid & 31;
   const int row = blockIdx.y;
-  if (tid == 0) s_n = 0;
+  if (tid == 0) s_group = kNone;
   pdl_wait_and_trigger();
   __syncthreads();
   for (int e = tid; e < a.E; e += kGvThreads) {
@@ -228,20 +232,17 @@ __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(
     if (lo < 0 || hi < lo || hi > a.rows) {
       set_status(MOE_ERR_DEVICE_INDEX);
     } else if (lo == row && hi > lo) {
-      int p = e, n = hi - lo;
-      if (a.slot_map) {
-        p = __ldg(a.slot_map + e);
-        if (p < 0 || p >= a.n_phys) {
-          if (p != -1) set_status(MOE_ERR_DEVICE_INDEX);
-          n = 0;  // not resident: its rows are left as they are
-        }
-      }
-      s_phys = p;
-      s_n = n;
+      const int p = a.slot_map ? __ldg(a.slot_map + e) : e;
+      if (p >= 0 && p < a.n_phys)
+        atomicMin(&s_group, ((unsigned long long)e << kRowBits | (unsigned)(hi - lo)) << kPhysBits | (unsigned)p);
+      else if (p != -1)  // (-1: not resident, its rows are left as they are)
+        set_status(MOE_ERR_DEVICE_INDEX);
     }
   }
   __syncthreads();
-  const int n = s_n, phys = s_phys, warp = tid >> 5;
+  const unsigned long long group = s_group;
+  const int phys = (int)(group & ((1ull << kPhysBits) - 1)), warp = tid >> 5;
+  const int n = group == kNone ? 0 : (int)(group >> kPhysBits & ((1u << kRowBits) - 1));
   const int ch0 = (kSplit ? blockIdx.x : blockIdx.x * kGvWarps + warp) * kGvChan;
   if (n == 0 || ch0 >= a.channels) return;
   int r = 0;

@@ -236,7 +236,8 @@ moe_status moe_layer_forward(const moe_layer_desc* desc, const void* x, const vo
  * of each expert e by that expert's matrix; offsets, and the order of the
  * rows, are what moe_permute writes.  Offsets have to be non-decreasing and
  * within [0, rows]; a pair that is not sets MOE_ERR_DEVICE_INDEX and counts as
- * an empty group.  Rows in no group (before offsets[0], behind offsets[E]),
+ * an empty group; a row that several pairs claim after that gets one of their
+ * results, it is not said whose.  Rows in no group (before offsets[0], behind offsets[E]),
  * and the rows of an expert that slot_map calls not resident (-1), are neither
  * read into any result nor written.
  *

@@ -1023,3 +1023,39 @@ def test_grad_w_of_a_very_long_group(ot):
     check(dw, ref, mag * (640 + 2 + R / 640) * U)
     if ot == FP32:
         assert (dw.double() - ref).norm() <= 4e-6 * ref.norm()
+
+
+# ------------------------------------- rows that several pairs of offsets claim
+
+@pytest.mark.parametrize("R,away", [(10, ()), (10, (0,)), (10, (0, 2, 4)), (300, ()), (300, (0, 6))])
+def test_rows_claimed_by_several_experts_get_one_of_their_products(R, away):
+    """Offsets that go back and forth, a matrix of its own for each expert, some of them not resident.  Few rows: the
+    lowest resident expert's product, whole, and the same again; many: element by element one of the claimants'."""
+    g = gen(31)
+    E, N, K = 16, 96, 72
+    off = torch.tensor([0, R - 3] * (E // 2) + [0], dtype=torch.int32, device=DEV)
+    slots = torch.tensor([-1 if e in away else E - 1 - e for e in range(E)], dtype=torch.int32, device=DEV)
+    x, w = normal((R, K), BF16, g), normal((E, N, K), BF16, g, 0.1)
+    claim = [e for e in range(0, E, 2) if e not in away]
+    refs = torch.stack([x[: R - 3].double() @ w[E - 1 - e].double().t() for e in claim])
+    mags = torch.stack([x[: R - 3].double().abs() @ w[E - 1 - e].double().abs().t() for e in claim])
+    for _ in range(20):
+        out = torch.full((R, N), 7.0, dtype=BF16, device=DEV)
+        moe.moe_grouped_gemm(x, w, off, out, slot_map=slots)
+        assert moe.moe_get_last_error() == 9
+        got = out[: R - 3].double()
+        if R == 10:
+            check(out[: R - 3], refs[0], mags[0] * (K + 2) * U)
+        else:
+            allowed = refs.abs() * half_step(BF16) + tiny(BF16) + mags * (K + 2) * U * (1 + half_step(BF16))
+            assert bool(((got - refs).abs() <= allowed).any(0).all())
+        assert bool((out[R - 3:] == 7.0).all())
+    q, wq = codes((R, K), g), codes((E, N, K), g)
+    sx, sw = torch.rand(R, generator=g, device=DEV), torch.rand(E, N, generator=g, device=DEV)
+    out = torch.full((R, N), 7.0, device=DEV)
+    moe.moe_grouped_gemm_i8(q, sx, wq, sw, off, out, slot_map=slots)
+    assert moe.moe_get_last_error() == 9
+    refs = torch.stack([(q[: R - 3].double() @ wq[E - 1 - e].double().t()) * sx[: R - 3].double()[:, None]
+                        * sw[E - 1 - e].double() for e in claim])
+    near = (out[: R - 3].double() - refs).abs() <= refs.abs() * 2.0 ** -22
+    assert bool((near[0] if R == 10 else near.any(0)).all())
