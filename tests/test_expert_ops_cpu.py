@@ -291,3 +291,53 @@ def test_fewer_matrices_than_experts_need_a_slot_map():
     assert _forward(_desc(rows=0, n_experts=4, n_physical=3)) == INVALID
     # (with one: nothing to do, and no complaint)
     assert L.moe_grouped_gemm(ctypes.byref(_desc(rows=0, n_experts=4, n_physical=3)), P, P, P, off, P, None) == 0
+
+
+def test_the_end_of_a_row_is_read_no_further(tmp_path):
+    """The few-row kernel's reads of a row's last bytes, as the host sees them: inside the row, on their alignment,
+    every byte once, zeros behind."""
+    import os
+    import subprocess
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "tail.cpp"
+    src.write_text(r"""
+#include "%s/expert_ffn_layer_route_b200/csrc/row_tail.cuh"
+#include <cstring>
+#include <cstdio>
+alignas(16) static uint8_t buf[32];
+static int n, seen[32], bad;
+struct Load {
+  template <typename T> T get(const uint8_t* p) const {
+    const int at = (int)(p - buf);
+    if (at %% (int)sizeof(T) || at < 0 || at + (int)sizeof(T) > n) ++bad;
+    for (unsigned i = 0; i < sizeof(T); ++i) ++seen[at + i];
+    T v;
+    std::memcpy(&v, p, sizeof(T));
+    return v;
+  }
+  uint32_t u32(const uint8_t* p) const { return get<uint32_t>(p); }
+  uint16_t u16(const uint8_t* p) const { return get<uint16_t>(p); }
+  uint8_t u8(const uint8_t* p) const { return get<uint8_t>(p); }
+};
+int main() {
+  for (int i = 0; i < 32; ++i) buf[i] = (uint8_t)(200 + i);
+  for (n = 0; n <= 16; ++n) {
+    std::memset(seen, 0, sizeof(seen));
+    uint8_t got[16];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = moe::tail_word(buf + 4 * i, n - 4 * i, Load());
+      std::memcpy(got + 4 * i, &w, 4);
+    }
+    for (int i = 0; i < 16; ++i)
+      if (got[i] != (i < n ? buf[i] : 0) || seen[i] != (i < n)) ++bad;
+  }
+  std::printf("%%d\n", bad);
+}
+""" % root)
+    exe = str(tmp_path / "tail")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", str(src), "-o", exe], check=True)
+    assert subprocess.run([exe], capture_output=True, text=True, check=True).stdout == "0\n"
+    # and the kernel has no other way to a row's end
+    text = open(os.path.join(root, "expert_ffn_layer_route_b200", "csrc", "grouped_gemv.cu")).read()
+    assert "tail_word" in text and "keep(" not in text
