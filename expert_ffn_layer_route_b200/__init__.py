@@ -44,4 +44,5 @@ from ._native import (  # noqa: F401
     moe_profile_enable,
     moe_profile_collect,
     moe_diag_wait_timeout,
+    moe_diag_wait_moving,
 )

@@ -101,6 +101,7 @@ _SIGS = {
     "moe_get_last_error": [],
     "moe_profile_enable": [ctypes.c_int],
     "moe_diag_wait_timeout": [ctypes.c_uint64, _P, _P],
+    "moe_diag_wait_moving": [ctypes.c_uint64, _I32, _I32, _P, _P],
     "moe_profile_collect": [ctypes.POINTER(ProfileEntry), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
 }
 _PTR_RET = {"moe_cache_host_expert": [_P, ctypes.c_int32, ctypes.c_int32],
@@ -477,6 +478,11 @@ def moe_get_last_error() -> int:
 
 def moe_diag_wait_timeout(limit_ns: int, finished, stream=None):
     _check(lib().moe_diag_wait_timeout(int(limit_ns), _ptr(finished), _stream(stream)), "moe_diag_wait_timeout")
+
+
+def moe_diag_wait_moving(limit_ns: int, moves: int, complete: bool, finished, stream=None):
+    _check(lib().moe_diag_wait_moving(int(limit_ns), moves, int(complete), _ptr(finished), _stream(stream)),
+           "moe_diag_wait_moving")
 
 
 def moe_profile_enable(on: bool = True):

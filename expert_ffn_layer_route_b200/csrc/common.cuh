@@ -37,8 +37,10 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
-// Limit for any single device-side wait.  Every legitimate wait in these
-// kernels ends within microseconds; two seconds only guards against a bug.
+// Limit for any single device-side wait.  A legitimate wait in these kernels is
+// for one step of a pipeline, a piece of a sum or a tile's results: microseconds.
+// Two seconds only guard against a bug.  A wait that spans many of those is
+// mbar_wait_moving, whose limit starts anew with each of them.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // ---------------------------------------------------------------- mbarrier
@@ -82,25 +84,46 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait for the phase with the given parity to complete.
+// Whether the phase with the given parity completes within the limit.
 template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   if (mbar_try_wait<kCluster>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait<kCluster>(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      set_status(MOE_ERR_TIMEOUT);
-      return false;
-    }
+    if (globaltimer_ns() - t0 > limit_ns) return false;
   }
+}
+
+// Bounded wait for the phase with the given parity to complete.
+template <bool kCluster = false>
+__device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_poll<kCluster>(bar, parity, limit_ns)) return true;
+  set_status(MOE_ERR_TIMEOUT);
+  return false;
 }
 
 template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return mbar_wait_limit<kCluster>(bar, parity, kWaitLimitNs);
+}
+
+// A whole warp's wait for something that many other steps may come before: it is
+// given up when *progress, which each step changes, has stood still for the limit.
+__device__ __forceinline__ bool mbar_wait_moving(uint64_t* bar, uint32_t parity, volatile int* progress,
+                                                 uint64_t limit_ns = kWaitLimitNs) {
+  int seen = __shfl_sync(0xffffffffu, *progress, 0);
+  while (!__all_sync(0xffffffffu, mbar_poll(bar, parity, limit_ns))) {
+    const int now = __shfl_sync(0xffffffffu, *progress, 0);
+    if (now == seen) {
+      set_status(MOE_ERR_TIMEOUT);
+      return false;
+    }
+    seen = now;
+  }
+  return true;
 }
 
 // ----------------------------------------------------------------- cluster

@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_ngroups = reinterpret_cast<int*>(s_tmem + 2);
+  volatile int* s_tile = reinterpret_cast<volatile int*>(s_tmem + 3);  // grad_w: the tile whose operands are being brought
   Group* grp = reinterpret_cast<Group*>(s_tmem + 6);  // [E + 1], the groups that have tiles
 
   if (tid == 0) {
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
     }
     mbar_init(drain, 1);
     *s_abort = 0;
+    *s_tile = -1;
     fence_barrier_init();
   }
   if (warp == 1) tc::tmem_alloc_g<kPair>(s_tmem, a.tmem_cols);
@@ -642,6 +644,7 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
     uint32_t s = 0, par = 1, cnt = 0, tails = 0, tail_use = 0;
     for (int t = unit; t < total_tiles; t += units) {
       if (warp_any(*s_abort)) break;
+      if (kKind == kGgGradW) *s_tile = t;
       const Tile ti = tile_at(t);
       const int depth = uni(depth_of(ti));
       const int ncols = uni(mma_cols(ti));
@@ -924,7 +927,8 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
       const int left = ti.n % kDepthBlock;
       if ((left & 15) == 0) continue;
       const uint32_t s = (cnt - 1) % a.stages;
-      if (warp_any(*s_abort) || !warp_wait(&tail[s], (uses >> s) & 1u)) {
+      // (any number of tiles without a ragged stage may come before this one)
+      if (warp_any(*s_abort) || !mbar_wait_moving(&tail[s], (uses >> s) & 1u, s_tile)) {
         *s_abort = 1;
         break;
       }

@@ -548,7 +548,38 @@ __global__ void wait_timeout_probe_kernel(uint64_t limit_ns, int* finished) {
     *finished = ok ? 2 : 1;
   }
 }
+
+// The same for the wait that goes on while something moves: warp 1 moves it
+// `moves` times, 0.6 limits apart, then completes the phase or leaves it.
+__global__ void wait_moving_probe_kernel(uint64_t limit_ns, int moves, int complete, int* finished) {
+  __shared__ uint64_t bar;
+  __shared__ int step;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_barrier_init();
+    step = 0;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const bool ok = mbar_wait_moving(&bar, 0, &step, limit_ns);
+    if (threadIdx.x == 0) *finished = ok ? 2 : 1;
+  } else if (threadIdx.x == 32) {
+    for (int i = 0; i <= moves; ++i) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < limit_ns / 10 * 6) __nanosleep(1000);
+      if (i < moves) *(volatile int*)&step = i + 1;
+    }
+    if (complete) mbar_arrive(&bar);
+  }
+}
 }  // namespace moe
+
+extern "C" moe_status moe_diag_wait_moving(uint64_t limit_ns, int32_t moves, int32_t complete, int32_t* finished,
+                                           void* stream) {
+  if (!finished || limit_ns > 1000000000ull || moves < 0 || moves > 10) return MOE_ERR_INVALID_ARG;
+  moe::wait_moving_probe_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns, moves, complete, finished);
+  return from_cuda(cudaGetLastError());
+}
 
 extern "C" moe_status moe_diag_wait_timeout(uint64_t limit_ns, int32_t* finished, void* stream) {
   if (!finished || limit_ns > 10000000000ull) return MOE_ERR_INVALID_ARG;

@@ -428,6 +428,11 @@ moe_status moe_profile_collect(moe_profile_entry* out, int32_t cap, int32_t* n_o
  * int32) and the kernel returns: the failure path of a stuck pipeline,
  * exercised without hanging or faulting the GPU. */
 moe_status moe_diag_wait_timeout(uint64_t limit_ns, int32_t* finished, void* stream);
+/* The same for the wait whose limit (<= 1 s) starts anew while the pipeline
+ * moves: something moves `moves` (<= 10) times, 0.6 limits apart, and then the
+ * phase completes (complete != 0; *finished becomes 2) or never does (1, and
+ * MOE_ERR_TIMEOUT). */
+moe_status moe_diag_wait_moving(uint64_t limit_ns, int32_t moves, int32_t complete, int32_t* finished, void* stream);
 
 const char* moe_status_string(moe_status s);
 /* Synchronises the current device, returns and clears the device status word. */

@@ -1059,3 +1059,34 @@ def test_rows_claimed_by_several_experts_get_one_of_their_products(R, away):
                         * sw[E - 1 - e].double() for e in claim])
     near = (out[: R - 3].double() - refs).abs() <= refs.abs() * 2.0 ** -22
     assert bool((near[0] if R == 10 else near.any(0)).all())
+
+
+# ------------------------------------------------- a wait that spans many tiles
+
+def test_a_wait_goes_on_while_the_pipeline_moves():
+    """grad_w's clearing warp waits for a group's ragged end, before which any number of whole tiles may come: its
+    limit starts anew with each; when nothing moves any more it gives up."""
+    import time
+
+    limit, flag = 50_000_000, torch.zeros(1, dtype=torch.int32, device=DEV)
+    moe.moe_get_last_error()
+    for moves, complete, finished, status in ((0, True, 2, 0), (6, True, 2, 0), (0, False, 1, 6), (4, False, 1, 6)):
+        t0 = time.perf_counter()
+        moe.moe_diag_wait_moving(limit, moves, complete, flag)
+        assert moe.moe_get_last_error() == status and flag.item() == finished
+        assert time.perf_counter() - t0 >= 0.6e-9 * limit * moves
+
+
+def test_grad_w_ragged_groups_behind_whole_ones():
+    """Many tiles of groups that are multiples of 16 rows before, between and after those of ragged ones, on every CTA."""
+    g = gen(32)
+    counts = [640, 0, 1280, 16, 7, 64, 64, 128, 48, 100, 0, 640, 1]
+    N, K = 520, 2100
+    off, R = offsets_of(counts), sum(counts)
+    dy, x = normal((R, N), BF16, g), normal((R, K), BF16, g)
+    for ot in (BF16, FP32):
+        dw = torch.full((len(counts), N, K), 7.0, dtype=ot, device=DEV)
+        moe.moe_grouped_gemm_grad_w(dy, x, off, dw)
+        ok()
+        ref, mag = ref_grad_w(dy, x, off)
+        check(dw, ref, mag * (640 + 2 + 2) * U)
