@@ -178,7 +178,8 @@ moe_status moe_quant_rows_i8(int32_t rows, int32_t K, int32_t dtype, const void*
   if (!ld_q) ld_q = K;
   if (ld_x < K || ld_q < K || (row_token && n_tokens < 0)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!x || !on(x, 2) || !q || !scale || !on(scale, 4) || (row_token && !on(row_token, 4))) return MOE_ERR_INVALID_ARG;
+  if (!x && !(row_token && n_tokens == 0)) return MOE_ERR_INVALID_ARG;  // (without tokens no source is read)
+  if (!on(x, 2) || !q || !scale || !on(scale, 4) || (row_token && !on(row_token, 4))) return MOE_ERR_INVALID_ARG;
   return from(launch_quant_rows(dtype, false, rows, K, x, ld_x, row_token, n_tokens, q, ld_q, scale,
                                 static_cast<cudaStream_t>(stream)));
 }

@@ -313,7 +313,8 @@ moe_status moe_grouped_gemm_i8(const moe_gemm_desc* desc, const int8_t* x, const
  * zeros with scale NaN, so that every product with it is NaN.
  * x: bf16 or fp16 (dtype) [n_tokens][K] of pitch ld_x; q int8 [rows][K] of
  * pitch ld_q; scale fp32 [rows]; pitches in elements, 0: K.  row_token: device
- * int32 [rows], or NULL (n_tokens is then not looked at). */
+ * int32 [rows], or NULL (n_tokens is then not looked at).  With n_tokens = 0
+ * x may be NULL: every row is a dropped one. */
 moe_status moe_quant_rows_i8(int32_t rows, int32_t K, int32_t dtype, const void* x, int64_t ld_x,
                              const int32_t* row_token, int32_t n_tokens, int8_t* q, int64_t ld_q, float* scale,
                              void* stream);

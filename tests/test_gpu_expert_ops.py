@@ -1090,3 +1090,13 @@ def test_grad_w_ragged_groups_behind_whole_ones():
         ok()
         ref, mag = ref_grad_w(dy, x, off)
         check(dw, ref, mag * (640 + 2 + 2) * U)
+
+
+@pytest.mark.parametrize("K", [8, 300, 5000])
+def test_rows_of_no_token_at_all(K):
+    """No tokens, and rows whose pairs were all dropped: zeros with scale 0, nothing is read."""
+    tok = torch.tensor([-1, 0, 5], dtype=torch.int32, device=DEV)
+    q, s = torch.full((3, K), 99, dtype=torch.int8, device=DEV), torch.full((3,), 99.0, device=DEV)
+    moe.moe_quant_rows_i8(torch.empty(0, K, dtype=BF16, device=DEV), q, s, row_token=tok)
+    ok()
+    assert not bool(q.any()) and not bool(s.any())
