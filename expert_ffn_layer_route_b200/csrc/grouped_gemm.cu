@@ -23,6 +23,7 @@
 // (1340-1400), 1.55 at the power limit; 256 rows of 128 experts, [5760][2880],
 // 0.51 ms (7.0 TB/s); int8, 1024 rows of 384 experts, [4096][7168], 0.98 ms (6.9
 // TB/s); grad_w in fp32, 8192 rows of 128 experts, [2880][2880], 0.77-0.86 ms.
+#include <atomic>
 #include <cstring>
 
 #include "grouped_gemm.cuh"
@@ -959,12 +960,14 @@ cudaError_t launch_as(const GgArgs& a, int grid, size_t smem, cudaStream_t st) {
   cudaError_t err = set_dyn_smem_once<grouped_gemm_kernel<kKind, kPair, kOut, kVec16>>(smem);
   if (err != cudaSuccess) return err;
   if (kKind == kGgGradW) {  // a warp would wait for registers for good if the compiler had given it fewer than that
-    static const bool as_planned = [] {
+    static std::atomic<bool> as_planned{false};
+    if (!as_planned.load(std::memory_order_relaxed)) {
       cudaFuncAttributes at;
-      return cudaFuncGetAttributes(&at, grouped_gemm_kernel<kKind, kPair, kOut, kVec16>) == cudaSuccess &&
-             at.numRegs == kLaunchRegs;
-    }();
-    if (!as_planned) return cudaErrorLaunchOutOfResources;
+      err = cudaFuncGetAttributes(&at, grouped_gemm_kernel<kKind, kPair, kOut, kVec16>);
+      if (err != cudaSuccess) return err;
+      if (at.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
+      as_planned.store(true, std::memory_order_relaxed);
+    }
   }
   static const char* const names[4] = {"grouped_gemm", "grouped_gemm_grad_x", "grouped_gemm_grad_w",
                                        "grouped_gemm_i8"};
