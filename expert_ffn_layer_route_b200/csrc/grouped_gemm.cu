@@ -356,11 +356,6 @@ __device__ __forceinline__ void put_line(const LineOut& w, int at, const uint32_
   }
 }
 
-__device__ __forceinline__ void clear_lines(const LineOut& w, int lane) {
-#pragma unroll
-  for (int z = 0; z < 8; ++z) reinterpret_cast<uint4*>(w.stage + lane * 128)[z ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
-}
-
 // The staged lines of column j0.
 template <int kOut, bool kVec16, int kMost, typename F>
 __device__ __forceinline__ void store_line(const LineOut& w, int j0, int lane, F between) {
@@ -379,6 +374,16 @@ __device__ __forceinline__ void store_line(const LineOut& w, int j0, int lane, F
     between();
   }
   __syncwarp();
+}
+
+// Zeros, for an expert without rows (out of line: there is nothing to keep in registers).
+template <int kOut, bool kVec16>
+__device__ __noinline__ void store_zeros(const LineOut w, int half, int lane) {
+  constexpr int kPerLine = kOut == k16 ? 64 : 32;
+#pragma unroll
+  for (int z = 0; z < 8; ++z) reinterpret_cast<uint4*>(w.stage + lane * 128)[z ^ (lane & 7)] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int j0 = half * kPerLine; j0 < w.nc; j0 += 2 * kPerLine) store_line<kOut, kVec16, 8>(w, j0, lane, [] {});
 }
 
 // What sums will be added to, on its way to L2 while the tile's products run:
@@ -834,6 +839,12 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
         // 128-byte lines, which the two warps of a quadrant take in turn
         constexpr int kPerLine = kF32 ? 32 : 64;
         if (kAdd && mine) prefetch_lines(w, half * kPerLine, 2 * kPerLine, lane);
+        if (!kAdd && ti.n == 0) {  // (with sums to add there is no such tile)
+          if (!acc.take()) break;
+          acc.release(lane);
+          if (mine) store_zeros<kOut, kVec16>(w, half, lane);
+          continue;
+        }
         if (ti.n <= kPiece) {
           // One piece: straight from the accumulator, the next line's values on their way while one leaves.  With few
           // rows to a group the epilogue is all there is.
@@ -845,15 +856,11 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
 #pragma unroll 1
             for (int j0 = first; j0 < ti.nc; j0 += 2 * kPerLine) {
               tc::ld_wait32(v);
-              if (ti.n == 0) {
-                clear_lines(w, lane);
-              } else {
-                put_line<kF32>(w, 0, v, lane);
-                if constexpr (!kF32) {
-                  tc::ld_issue32(acc.addr() + j0 + 32, v);
-                  tc::ld_wait32(v);
-                  put_line<kF32>(w, 4, v, lane);
-                }
+              put_line<kF32>(w, 0, v, lane);
+              if constexpr (!kF32) {
+                tc::ld_issue32(acc.addr() + j0 + 32, v);
+                tc::ld_wait32(v);
+                put_line<kF32>(w, 4, v, lane);
               }
               // (8 loads at a time where the registers allow it)
               store_line<kOut, kVec16, kOut == kF32Out && kVec16 ? 4 : 8>(w, j0, lane, [&] {
