@@ -22,12 +22,15 @@ namespace moe {
 
 namespace {
 
-// 24 warps of 85 registers on an SM.  gpt-oss-shaped gate/up, one token / two
+// 24 warps of 80 registers on an SM; in int8 some 100 bytes a thread go through
+// local memory for that, and where rows do not end on 16 bytes 20 warps of 96 are
+// the better ones (10 rows of 84 experts, [2145][3555], 17.3 us, 16.0; but not in
+// 16 bits: 5 rows, [1275][10201], 18.3, 19.9).  gpt-oss-shaped gate/up, one token / two
 // tokens in bf16, in int8 with its quantisation, and one expert alone in int8:
 // 24.0 / 45.5, 16.2 / 28.0, 6.3 us; 3 blocks of 256 24.4 / 46.4, 16.5 / 28.6, 6.3;
 // 10 blocks of 128 (fewer registers) 24.4 / 43.8, 15.8 / 26.9, 7.6.
 constexpr int kGvThreads = 128;
-constexpr int kGvMinBlocks = 6;
+constexpr int gv_min_blocks(int type, bool tail) { return type == MOE_T_INT8 && tail ? 5 : 6; }
 constexpr int kGvChan = 4;                             // channels per warp
 constexpr int kGvWarps = kGvThreads / 32;
 
@@ -56,16 +59,42 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
   return v;
 }
 
-struct LoadTail {
-  __device__ __forceinline__ uint32_t u32(const uint8_t* p) const { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
-  __device__ __forceinline__ uint16_t u16(const uint8_t* p) const { return __ldg(reinterpret_cast<const uint16_t*>(p)); }
-  __device__ __forceinline__ uint8_t u8(const uint8_t* p) const { return __ldg(p); }
+struct LoadTail {  // (predicated: 0 where nothing is to be read)
+  __device__ __forceinline__ uint32_t u32(const uint8_t* p, bool on) const {
+    uint32_t v;
+    asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %2, 0;\n mov.u32 %0, 0;\n @q ld.global.nc.u32 %0, [%1];\n}\n"
+                 : "=&r"(v) : "l"(p), "r"((uint32_t)on));
+    return v;
+  }
+  __device__ __forceinline__ uint32_t u16(const uint8_t* p, bool on) const {
+    uint32_t v;
+    asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %2, 0;\n mov.u32 %0, 0;\n @q ld.global.nc.u16 %0, [%1];\n}\n"
+                 : "=&r"(v) : "l"(p), "r"((uint32_t)on));
+    return v;
+  }
+  __device__ __forceinline__ uint32_t u8(const uint8_t* p, bool on) const {
+    uint32_t v;
+    asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %2, 0;\n mov.u32 %0, 0;\n @q ld.global.nc.u8 %0, [%1];\n}\n"
+                 : "=&r"(v) : "l"(p), "r"((uint32_t)on));
+    return v;
+  }
 };
-// The last n < 16 bytes of a row, zeros behind them: what lies there may be anything, or no memory at all.
+// The last n < 16 bytes of a row, zeros behind them, and no read behind them.
 __device__ __forceinline__ uint4 load_tail(const uint8_t* p, int n) {
   const LoadTail load;
   return make_uint4(tail_word(p, n, load), tail_word(p + 4, n - 4, load), tail_word(p + 8, n - 8, load),
                     tail_word(p + 12, n - 12, load));
+}
+// The first n bytes of a 16-byte piece, zeros behind them (what lies behind a
+// row's end may be anything, a NaN too).
+__device__ __forceinline__ uint4 keep(uint4 v, int n) {
+  uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = n - 4 * i;
+    e[i] = b >= 4 ? e[i] : b <= 0 ? 0u : e[i] & (0xffffffffu >> (32 - 8 * b));
+  }
+  return v;
 }
 
 template <int kType>
@@ -159,20 +188,33 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
     dot<kType, R>(w0, x0, acc);
     dot<kType, R>(w1, x1, acc);
   }
-  for (; b < whole; b += kStep) {
+  // A row's last bytes, fewer than 16 (kTail), come with the bytes up to the next 16, which every row but a buffer's
+  // last one has behind it by its pitch; those of a last one by themselves.
+  const bool w_ends = kTail && phys == a.n_phys - 1 && ch0 + kGvChan >= a.channels;
+  const bool x_ends = kTail && row + R == a.rows;
+  for (; b < a.depth_bytes; b += kStep) {
+    const int n = a.depth_bytes - b;
     uint4 w0[kGvChan], x0[R];
+    if (kTail && w_ends && n < 16) {
 #pragma unroll
-    for (int c = 0; c < kGvChan; ++c) w0[c] = load_stream(w[c] + b);
+      for (int c = 0; c < kGvChan; ++c) w0[c] = load_tail(w[c] + b, n);
+    } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r) x0[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b));
-    dot<kType, R>(w0, x0, acc);
-  }
-  if (kTail && b < a.depth_bytes) {  // one lane: the row's last bytes, fewer than 16
-    uint4 w0[kGvChan], x0[R];
+      for (int c = 0; c < kGvChan; ++c) w0[c] = load_stream(w[c] + b);
+    }
+    if (kTail && x_ends && n < 16) {
 #pragma unroll
-    for (int c = 0; c < kGvChan; ++c) w0[c] = load_tail(w[c] + b, a.depth_bytes - b);
+      for (int r = 0; r < R; ++r) x0[r] = load_tail(x[r] + b, n);
+    } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r) x0[r] = load_tail(x[r] + b, a.depth_bytes - b);
+      for (int r = 0; r < R; ++r) x0[r] = __ldg(reinterpret_cast<const uint4*>(x[r] + b));
+    }
+    if (kTail && n < 16) {
+#pragma unroll
+      for (int c = 0; c < kGvChan; ++c) w0[c] = keep(w0[c], n);
+#pragma unroll
+      for (int r = 0; r < R; ++r) x0[r] = keep(x0[r], n);
+    }
     dot<kType, R>(w0, x0, acc);
   }
 #pragma unroll
@@ -221,12 +263,11 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
 // whole group, those of its other rows end at once, so that a group's weights
 // are read once whatever the routing.
 template <int kType, bool kSplit, bool kTail>
-__global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(const GemvArgs a) {
-  // The group that starts at the block's row: expert, rows and matrix in one word, the lowest expert's if offsets
-  // that go back and forth claim the row for several.
-  constexpr int kPhysBits = 31, kRowBits = 8;
-  constexpr unsigned long long kNone = ~0ull;
-  __shared__ unsigned long long s_group;
+__global__ void __launch_bounds__(kGvThreads, gv_min_blocks(kType, kTail)) grouped_gemv_kernel(const GemvArgs a) {
+  // The group that starts at the block's row, its expert and rows in one word: the lowest resident expert's, where
+  // offsets that go back and forth claim the row for several.
+  constexpr int kRowBits = 8, kNone = 0x7fffffff;
+  __shared__ int s_group;
   const int tid = threadIdx.x, lane = tid & 31;
   const int row = blockIdx.y;
   if (tid == 0) s_group = kNone;
@@ -239,17 +280,18 @@ __global__ void __launch_bounds__(kGvThreads, kGvMinBlocks) grouped_gemv_kernel(
     } else if (lo == row && hi > lo) {
       const int p = a.slot_map ? __ldg(a.slot_map + e) : e;
       if (p >= 0 && p < a.n_phys)
-        atomicMin(&s_group, ((unsigned long long)e << kRowBits | (unsigned)(hi - lo)) << kPhysBits | (unsigned)p);
+        atomicMin(&s_group, e << kRowBits | (hi - lo));
       else if (p != -1)  // (-1: not resident, its rows are left as they are)
         set_status(MOE_ERR_DEVICE_INDEX);
     }
   }
   __syncthreads();
-  const unsigned long long group = s_group;
-  const int phys = (int)(group & ((1ull << kPhysBits) - 1)), warp = tid >> 5;
-  const int n = group == kNone ? 0 : (int)(group >> kPhysBits & ((1u << kRowBits) - 1));
+  const int group = s_group, warp = tid >> 5;
+  if (group == kNone) return;
+  const int n = group & ((1 << kRowBits) - 1), expert = group >> kRowBits;
+  const int phys = a.slot_map ? __ldg(a.slot_map + expert) : expert;
   const int ch0 = (kSplit ? blockIdx.x : blockIdx.x * kGvWarps + warp) * kGvChan;
-  if (n == 0 || ch0 >= a.channels) return;
+  if (ch0 >= a.channels) return;
   int r = 0;
   for (; r + 2 <= n; r += 2) rows_of<kType, 2, kSplit, kTail>(a, row + r, ch0, phys, warp, lane);
   if (r < n) rows_of<kType, 1, kSplit, kTail>(a, row + r, ch0, phys, warp, lane);

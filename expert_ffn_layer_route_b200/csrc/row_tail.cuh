@@ -13,17 +13,15 @@
 
 namespace moe {
 
-// Bytes [0, left) of the 4-byte word at p (any left), zeros behind them; read by
-// load.u32, .u16 and .u8, each at an address that is a multiple of its size if p is.
+// Bytes [0, left) of the 4-byte word at p (any left), zeros behind them, by
+// load.u32, .u16 and .u8(address, whether to read: 0 if not), each at a multiple
+// of its size if p is one of 4.  No branches: a thread's reads are on their way
+// together.
 template <typename Load>
 MOE_HOST_DEVICE uint32_t tail_word(const uint8_t* p, int left, const Load& load) {
-  if (left >= 4) return load.u32(p);
-  uint32_t v = 0;
-  if (left > 0) {
-    if (left & 2) v = load.u16(p);
-    if (left & 1) v |= (uint32_t)load.u8(p + (left & 2)) << (8 * (left & 2));
-  }
-  return v;
+  const bool part = left > 0 && left < 4;
+  return load.u32(p, left >= 4) | load.u16(p, part && (left & 2)) |
+         load.u8(p + (left & 2), part && (left & 1)) << (8 * (left & 2));
 }
 
 }  // namespace moe
