@@ -22,15 +22,15 @@ namespace moe {
 
 namespace {
 
-// 24 warps of 80 registers on an SM; in int8 some 100 bytes a thread go through
-// local memory for that, and where rows do not end on 16 bytes 20 warps of 96 are
-// the better ones (10 rows of 84 experts, [2145][3555], 17.3 us, 16.0; but not in
-// 16 bits: 5 rows, [1275][10201], 18.3, 19.9).  gpt-oss-shaped gate/up, one token / two
-// tokens in bf16, in int8 with its quantisation, and one expert alone in int8:
-// 24.0 / 45.5, 16.2 / 28.0, 6.3 us; 3 blocks of 256 24.4 / 46.4, 16.5 / 28.6, 6.3;
-// 10 blocks of 128 (fewer registers) 24.4 / 43.8, 15.8 / 26.9, 7.6.
+// 24 warps of 80 registers on an SM, in int8 20 of 96: with 80 some 100 bytes a
+// thread go through local memory there (gpt-oss-shaped gate/up with its
+// quantisation, one token / two tokens 16.5 / 28.3 us, 17.9 / 31.5; 10 rows of 84
+// experts, [2145][3555], 16.0, 17.3), in 16 bits nothing does (5 rows, [1275][10201],
+// 18.3 us, by 96 registers 19.9).  Blocks of 128 threads: gate/up in bf16, one token /
+// two tokens, and one expert alone in int8 24.0 / 45.5, 6.3 us; 3 blocks of 256 24.4
+// / 46.4, 6.3; 10 blocks of 128 (fewer registers) 24.4 / 43.8, 7.6.
 constexpr int kGvThreads = 128;
-constexpr int gv_min_blocks(int type, bool tail) { return type == MOE_T_INT8 && tail ? 5 : 6; }
+constexpr int gv_min_blocks(int type) { return type == MOE_T_INT8 ? 5 : 6; }
 constexpr int kGvChan = 4;                             // channels per warp
 constexpr int kGvWarps = kGvThreads / 32;
 
@@ -263,7 +263,7 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int64_t row, int ch0,
 // whole group, those of its other rows end at once, so that a group's weights
 // are read once whatever the routing.
 template <int kType, bool kSplit, bool kTail>
-__global__ void __launch_bounds__(kGvThreads, gv_min_blocks(kType, kTail)) grouped_gemv_kernel(const GemvArgs a) {
+__global__ void __launch_bounds__(kGvThreads, gv_min_blocks(kType)) grouped_gemv_kernel(const GemvArgs a) {
   // The group that starts at the block's row, its expert and rows in one word: the lowest resident expert's, where
   // offsets that go back and forth claim the row for several.
   constexpr int kRowBits = 8, kNone = 0x7fffffff;
