@@ -17,12 +17,14 @@
 // Roles of a CTA: warp 0 brings the operands (TMA, a ring of stages), warp 1
 // issues the MMAs, 4 warps (8 in tiles of more than 64 columns) take the sums and
 // write results, and in grad_w one more clears the ragged ends of groups; two
-// accumulators, so that one is read under the next one's products.  Measured (B200, HBM copy 6.56 TB/s, cuBLAS bf16 1.61
-// PFLOP/s in short runs, 1.37 at the power limit): 2048 x 28672 x 4096 bf16 329 us
-// (1460 TFLOP/s); 8192 ragged rows of 8 experts, the same matrices, 1.37-1.44 ms
-// (1340-1400), 1.55 at the power limit; 256 rows of 128 experts, [5760][2880],
-// 0.51 ms (7.0 TB/s); int8, 1024 rows of 384 experts, [4096][7168], 0.98 ms (6.9
-// TB/s); grad_w in fp32, 8192 rows of 128 experts, [2880][2880], 0.77-0.86 ms.
+// accumulators, so that one is read under the next one's products.
+// Measured (B200, HBM copy 6.56 TB/s, cuBLAS bf16 1.61 PFLOP/s in short runs, 1.37
+// at the power limit): 2048 x 28672 x 4096 bf16 314 us cold (1530 TFLOP/s); 8192
+// ragged rows of 8 experts, the same matrices, 1.39-1.44 ms (1335-1385), 1.59 at
+// the power limit; fp32 results 1.29-1.45 ms for even groups (of 16 bits 1.25-1.29);
+// 256 rows of 128 experts, [5760][2880], 0.52 ms (6.8 TB/s); int8, 1024 rows of 384
+// experts, [4096][7168], 0.98 ms (6.9 TB/s); grad_w in fp32, 8192 rows of 128
+// experts, [2880][2880], 0.77-0.88 ms, added 2.2 ms.
 #include <atomic>
 #include <cstring>
 
@@ -66,7 +68,7 @@ constexpr int gg_threads(int kind, bool pair) { return 32 * (first_epi(kind) + e
 // cache worth the name beside this shared memory (fp32 gradients of 128 experts
 // with 64 rows each: 1500 us).
 constexpr int kLaunchRegs = 168, kIssueRegs = 56, kEpiRegs = 224;
-static_assert(kIssueRegs + 2 * kEpiRegs == 3 * kLaunchRegs, "what the warpgroups have together is what they were launched with");
+static_assert(kIssueRegs + 2 * kEpiRegs == 3 * kLaunchRegs, "the warpgroups have what they were launched with");
 constexpr int kSingleCols = 64;  // widest tile of one CTA (but grad_w)
 enum { k16, kF32Out, kF32Add };  // result: a 16-bit type, fp32, (grad_w) fp32 added to what is there
 constexpr int kBoxBig = 64, kBoxSmall = 16;  // rows of the two TMA boxes of the ragged operand
@@ -464,7 +466,8 @@ __device__ __forceinline__ bool take_sums(Accumulators<kPair>& acc, uint32_t (&s
 
 // grad_w, a tile of several pieces: the accumulators taken so far, or -1 (given up).
 template <bool kPair, int kOut, bool kVec16>
-__device__ __forceinline__ int store_by_sums(Accumulators<kPair> acc, const LineOut w, int depth, int half, bool mine, int lane) {
+__device__ __forceinline__ int store_by_sums(Accumulators<kPair> acc, const LineOut w, int depth, int half, bool mine,
+                                             int lane) {
   constexpr bool kF32 = kOut != k16;
   constexpr int kPerLine = kF32 ? 32 : 64, kChunks = 4, kChunkLine = kPerLine / 32;
   uint32_t sum[kChunks][32];
@@ -506,7 +509,8 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
   constexpr int kDepthBlock = kLine / kElem;  // contraction elements per block
   constexpr int kDepthMma = 32 / kElem;
   constexpr int kColRound = kPair ? 32 : 16;
-  constexpr int kEpiBytes = epi_bytes(kKind, kOut != k16), kEpiWarps = epi_warps(kKind, kPair), kFirstEpi = first_epi(kKind);
+  constexpr int kEpiBytes = epi_bytes(kKind, kOut != k16), kEpiWarps = epi_warps(kKind, kPair);
+  constexpr int kFirstEpi = first_epi(kKind);
   constexpr int kTileChan = kPair ? 2 * kChan : kChan;
   constexpr bool kInPieces = kKind != kGgInt8, kF32 = kOut != k16, kAdd = kOut == kF32Add;
 
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_ngroups = reinterpret_cast<int*>(s_tmem + 2);
-  volatile int* s_tile = reinterpret_cast<volatile int*>(s_tmem + 3);  // grad_w: the tile whose operands are being brought
+  volatile int* s_tile = reinterpret_cast<volatile int*>(s_tmem + 3);  // grad_w: the tile that is being brought
   Group* grp = reinterpret_cast<Group*>(s_tmem + 6);  // [E + 1], the groups that have tiles
 
   if (tid == 0) {
@@ -881,22 +885,27 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
         // rows; through shared memory a row's channels leave side by side.
         // Two warps to a quadrant take turns at 32 rows.
         constexpr int kHalves = kEpiWarps / 4, kChunks = (kPair ? 256 : kSingleCols) / 32 / kHalves;
+        const int64_t row0 = (int64_t)ti.row0 + ti.c0;
+        // (the scales come while the products run)
+        float sw = 0.f, sx[kChunks] = {};
+        if constexpr (kKind == kGgInt8) {
+          if (ch0 + lane < a.channels) sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const int j = (half + kHalves * c) * 32 + lane;
+            if (j < ti.nc) sx[c] = __ldg(a.x_scale + row0 + j);
+          }
+        }
         uint32_t sum[kChunks][32];
         if (!take_sums<kInPieces, kPair, kChunks>(acc, sum, a.depth, ti.nc, mine, lane,
                                                   [&](int c) { return (half + kHalves * c) * 32; }))
           break;
         if (!mine) continue;
         constexpr int kRow = 32 * osz;
-        float sw = 0.f;
-        if (kKind == kGgInt8 && ch0 + lane < a.channels)
-          sw = __ldg(a.w_scale + (int64_t)ti.phys * a.channels + ch0 + lane);
-        const int64_t row0 = (int64_t)ti.row0 + ti.c0;
         const int width = min(32, a.channels - ch0) * osz;
         const int64_t op = a.ldo * osz;
 #pragma unroll 1
         for (int l = 0, j0 = half * 32; l < kChunks && j0 < ti.nc; ++l, j0 += 32 * kHalves) {
-          float sx = 0.f;
-          if (kKind == kGgInt8 && j0 + lane < ti.nc) sx = __ldg(a.x_scale + row0 + j0 + lane);
           const int n = min(32, ti.nc - j0);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {  // (registers have no index: the chunk by comparison)
@@ -907,7 +916,7 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
 #pragma unroll
               for (int j = g; j < g + 8; ++j) {
                 float f = __uint_as_float(sum[c][j]);
-                if constexpr (kKind == kGgInt8) f = (float)(int)sum[c][j] * (__shfl_sync(0xffffffffu, sx, j) * sw);
+                if constexpr (kKind == kGgInt8) f = (float)(int)sum[c][j] * (__shfl_sync(0xffffffffu, sx[c], j) * sw);
                 if constexpr (osz == 4)
                   *reinterpret_cast<float*>(stage_o + j * kRow + lane * 4) = f;
                 else
@@ -1083,6 +1092,7 @@ cudaError_t launch_grouped_gemm(const GroupedProblem& p, int n_sms, int smem_max
     cap /= 2;
     pair = pair && cap >= 128;
   }
+  if (!gw && !pair && cap > kSingleCols) cap = kSingleCols;  // (as the rules above have it: a thread holds no more)
   a.col_cap = cap;
   a.col_step = gw ? 64 : pair ? 32 : 16;
   const int64_t col_tiles = gw ? p.E * div_up(p.K, cap) : groups + p.rows / cap;
