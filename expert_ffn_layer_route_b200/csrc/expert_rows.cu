@@ -7,8 +7,10 @@
 //   codes of a row v: amax = max|v|, scale = amax / 127, inv = 127 / amax (two
 //   fp32 divisions), q = round-to-nearest-even(v inv) clamped to +-127
 // All sums, products and statistics are fp32.  Every value is read once and
-// written once: these kernels are bound by HBM (8192 x 14336: SwiGLU 110 us, its
-// gradient 167 us, 6.4 and 7.0 TB/s), the int8 rows by the latencies of a row.
+// written once.  SwiGLU and its gradient are bound by HBM (8192 x 14336: 109 and
+// 168 us, 6.5 and 7.0 TB/s); the int8 rows by the latencies of a row (8192 x 4096:
+// 34 us, 3.0 TB/s), those from SwiGLU also by their exactly rounded steps (8192 x
+// 14336: 180 us, 3.3 TB/s).
 #include "expert_rows.cuh"
 
 #include <algorithm>
@@ -92,8 +94,13 @@ __device__ __forceinline__ void store(T* p, const float (&v)[W]) {
   }
 }
 
-// exp and the quotient by the fast approximations (a few fp32 ulps): their
-// error is far below half a step of the 16-bit results and of the codes.
+// exp and the quotient by the fast approximations.  The first is off by 2 + 1.173
+// |g| units in the last place (some 100 at g = -87), the second by 2: 1e-5 at most,
+// well below half a step of the 16-bit results.  Codes are not made this way, as
+// it turns over those that lie next to a border (row_values).  Below g = -87.3 the
+// quotient is 0; to keep e^g in factors there costs what would else be HBM's time
+// (the gradient included, 8192 x 14336: 335 us, 287 where only vectors with such a
+// value do it, 267).
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -258,9 +265,10 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 // L1/L2.  A row's loads, its maximum and its stores come one after the other, so
 // what fills an SM is rows side by side: small blocks, 8 of 128 threads (3 of 384
 // for long rows).  Measured: 8192 rows of 4096, 34 us against 45 with 2 blocks of
-// 512; SwiGLU of 8192 x 14336 into codes 134 us (4.4 TB/s) against 154 (180 with
-// the exactly rounded steps that it takes now).  A persistent block that copies
-// rows ahead into shared memory took 60 and 140 us.
+// 512; SwiGLU of 8192 x 14336 into codes 180 us (by fast steps, that turn some codes
+// over, 134 against 154; 48 bytes a thread of that instance go through local
+// memory).  A persistent block that copies rows ahead into shared memory took 60
+// and, by fast steps, 140 us.
 template <typename T, bool kSwiglu, int W, int V, int NT>
 __global__ void __launch_bounds__(NT, NT == 384 ? 3 : 1024 / NT)
     quant_rows_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ row_token, int n_tokens,
