@@ -369,7 +369,7 @@ __device__ __forceinline__ void store_line(const LineOut& w, int j0, int lane, F
   if (!kAdd && kVec16 && width == 128) {
     between();
     store_lines<8, kMost>(w.out + j0 * osz, w.pitch, w.n, lane,
-                   [&](int r, int p) { return staged + r * 128 + ((p ^ (r & 7)) << 4); });
+                          [&](int r, int p) { return staged + r * 128 + ((p ^ (r & 7)) << 4); });
   } else {
     store_any<osz, 128, true, kAdd, kVec16, kMost>(w.out + j0 * osz, w.pitch, staged, w.n, width, w.vec, lane);
     __syncwarp();
@@ -425,7 +425,7 @@ struct Accumulators {
   }
 };
 
-// A tile's sums to registers, the pieces (of a depth of kPiece or less) added one
+// A tile's sums to registers, the pieces (kPiece products or fewer) added one
 // after the other: kChunks times 32 columns, from column(c) on where that is
 // below nc.  wanted: whether the warp's channels exist.  False: given up.
 template <bool kInPieces, bool kPair, int kChunks, typename Column>
@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(gg_threads(kKind, kPair), 1) grouped_gemm_kern
   } else if (warp >= kFirstEpi) {
     if constexpr (kKind == kGgGradW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ================================================================ epilogue
-    const int q = warp & 3;              // TMEM lane quadrant of this warp
-    const int half = (warp - kFirstEpi) >> 2;    // of two warps to a quadrant: which
+    const int q = warp & 3;                    // TMEM lane quadrant of this warp
+    const int half = (warp - kFirstEpi) >> 2;  // of two warps to a quadrant: which
     uint8_t* stage_o = epi + (warp - kFirstEpi) * kEpiBytes;
     const uint32_t staged = smem_u32(stage_o);
     constexpr int osz = kF32 ? 4 : 2;
